@@ -222,6 +222,95 @@ int mmq_q6K_prep_q8_sk(const void* wp, const void* xq, float* y, int64_t M, int6
 int mmq_q6K_exp_q8_sk(const void* we, const void* xq, float* y, int64_t M, int64_t N, int64_t K, void* ws,
                       size_t ws_bytes, qpg_stream_t stream);
 
+/*
+ * Microscaled 4-bit floating point (MXFP4): quantisation and product.
+ *
+ *   MXFP4 buffer ("xm", "w") of rows x K values, K % 32 == 0, qpg_mxfp4_bytes(rows, K) bytes, two planes:
+ *       bytes [0, rows*K/2):  codes, row-major; byte b of a row holds element 2b in its low
+ *                             nibble and 2b + 1 in its high nibble. A code is a sign bit (8) and
+ *                             one of 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *       then rows*K/32 bytes: scales [rows][K/32], e = 2^(e - 127), 255 = NaN.
+ *     16-byte aligned. Activations and weights have the same layout; the matrices of E experts
+ *     are one buffer of E*N rows.
+ *
+ * Element types of float arguments (x_type, y_type, ...): QPG_F32, QPG_F16, QPG_BF16; any other
+ * value is QPG_EINVAL. Arithmetic and sums are f32; a result is rounded once, to nearest
+ * even, when it is stored. Shapes of this section: 1 <= M, N < 2^31; 32 <= K <= 2^24,
+ * K % 32 == 0 (K / 32 need not be even or a multiple of anything); the number of tiles of
+ * 16 x 16 outputs must be < 2^31.
+ */
+enum { QPG_F32 = 0, QPG_F16 = 1, QPG_BF16 = 2 };
+
+/* rows*K/2 + rows*K/32; 0 for an unsupported shape (rows < 1, rows >= 2^31, K as above, rows*K >= 2^40). */
+size_t qpg_mxfp4_bytes(int64_t rows, int64_t K);
+
+/*
+ * quantize_mxfp4: x [M][K] -> xm. Per 32 values: e = max(floor(log2(max|x|)) - 2 + 127, 0)
+ * (0 for a block of zeros); code = x / 2^(e - 127) rounded to the nearest code, ties to
+ * the even one, magnitudes above 6 to 6; the sign of zero is kept. A block with a NaN or an
+ * infinity gets e = 255 and zero codes: all 32 values stand for NaN.
+ * dequantize_mxfp4: xm -> y [M][K], the values the codes stand for (exact in f32 and bf16
+ * below their overflow; f16 rounds). x, y and xm 16-byte aligned.
+ */
+int quantize_mxfp4(const void* x, int x_type, void* xm, int64_t M, int64_t K, qpg_stream_t stream);
+int dequantize_mxfp4(const void* xm, void* y, int y_type, int64_t M, int64_t K, qpg_stream_t stream);
+
+/*
+ * mmq_mxfp4_mx: y [M][N] = xm [M][K] x w [N][K]^T, both MXFP4; the products of codes are exact,
+ * summed in f32 on the scaled matrix instructions. A NaN scale makes the outputs of its row NaN.
+ * mmq_mxfp4: the same from float activations x; enqueues quantize_mxfp4 into the caller's
+ * workspace xm_ws (qpg_mxfp4_bytes(M, K) bytes, 16-byte aligned), then the product. After the
+ * stream has reached it, xm_ws holds MXFP4(x). Calls that share xm_ws must not overlap in time.
+ * x 16-byte aligned, y aligned to its element.
+ */
+int mmq_mxfp4_mx(const void* w, const void* xm, void* y, int y_type, int64_t M, int64_t N, int64_t K,
+                 qpg_stream_t stream);
+int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int64_t M, int64_t N, int64_t K,
+              void* xm_ws, qpg_stream_t stream);
+
+/*
+ * Experts: T tokens, top_k choices each; slot t*top_k + j is token t's j-th choice. S = T*top_k
+ * slots, 1 <= S < 2^31, 1 <= E <= 1024 experts.
+ *
+ * experts_sort: ids [S] (int32 or int64: id_bytes 4 or 8) -> the slots sorted by expert, stable.
+ *   offsets int32 [E + 1]: rows [offsets[e], offsets[e + 1]) of the sorted order are expert e's;
+ *   order   int32 [S]: slot of each row, -1 from row offsets[E] on;
+ *   slots   int32 [S]: row of each slot, or -1: an id outside [0, E) is no expert of this call,
+ *           its slot has no row. The same expert may be chosen twice by a token.
+ *   ws: qpg_experts_sort_bytes(S, E) bytes of scratch, 4-byte aligned (null when 0). Calls that
+ *   share ws must not overlap in time. ids aligned to its element; arrays 4 bytes.
+ *
+ * mmq_mxfp4_experts: y [S][N]; for each row p < offsets[E], of expert e,
+ *   y[p] = xm[order[p] / top_k] x w[e]^T, or xm[p] x w[e]^T with order null (activations already
+ *   in sorted order; then rows == S). w: MXFP4 of E*N rows, xm: MXFP4 of `rows` rows. Rows of
+ *   y from offsets[E] on are left as they were. offsets and order are read on the device: values
+ *   outside their ranges are clamped to them, so a wrong array gives wrong rows, never an access
+ *   outside the buffers.
+ *
+ * experts_gather: xs [S][H], xs[slots[t][j]] = x[t]; rows that no slot has are left as they were.
+ * experts_combine: y[t] = sum over j of weights[t][j] * ys[slots[t][j]], j upwards, in f32; slots
+ *   without a row add nothing. weights f32 [S], or null for ones: that is the gradient of
+ *   experts_gather, dx[t] = sum over j of dxs[slots[t][j]].
+ * experts_combine_grad: dys[slots[t][j]] = weights[t][j] * dy[t] (of ys's type; other rows left as
+ *   they were) and dweights f32 [S], dweights[t][j] = <dy[t], ys[slots[t][j]]>, 0 without a row.
+ *   In these three, a slots entry outside [0, S) counts as no row; two slots must not name one
+ *   row. H >= 1, H < 2^31; any element alignment; 16-byte aligned rows are faster. Outputs
+ *   must not overlap inputs.
+ */
+size_t qpg_experts_sort_bytes(int64_t S, int64_t E);
+int experts_sort(const void* ids, int id_bytes, int64_t S, int64_t E, int32_t* offsets, int32_t* order,
+                 int32_t* slots, void* ws, qpg_stream_t stream);
+int mmq_mxfp4_experts(const void* w, const void* xm, int64_t rows, const int32_t* offsets, const int32_t* order,
+                      int64_t top_k, void* y, int y_type, int64_t S, int64_t E, int64_t N, int64_t K,
+                      qpg_stream_t stream);
+int experts_gather(const void* x, int type, const int32_t* slots, void* xs, int64_t T, int64_t top_k, int64_t H,
+                   qpg_stream_t stream);
+int experts_combine(const void* ys, int ys_type, const int32_t* slots, const float* weights, void* y, int y_type,
+                    int64_t T, int64_t top_k, int64_t H, qpg_stream_t stream);
+int experts_combine_grad(const void* dy, int dy_type, const void* ys, int ys_type, const int32_t* slots,
+                         const float* weights, void* dys, float* dweights, int64_t T, int64_t top_k, int64_t H,
+                         qpg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -65,6 +65,18 @@ def lib() -> ctypes.CDLL:
                   L.mmq_q6K_isums, L.q6K_prepare, L.mmq_q6K_prep_q8, L.mmq_q6K_prep_isums, L.q6K_expand,
                   L.mmq_q6K_exp_q8, L.mmq_q6K_exp_csums):
             f.restype = ctypes.c_int
+        INT, SIZE = ctypes.c_int, ctypes.c_size_t
+        for f, res, args in (
+                (L.qpg_mxfp4_bytes, SIZE, [I64, I64]), (L.qpg_experts_sort_bytes, SIZE, [I64, I64]),
+                (L.quantize_mxfp4, INT, [P, INT, P, I64, I64, P]), (L.dequantize_mxfp4, INT, [P, P, INT, I64, I64, P]),
+                (L.mmq_mxfp4_mx, INT, [P, P, P, INT, I64, I64, I64, P]),
+                (L.mmq_mxfp4, INT, [P, P, INT, P, INT, I64, I64, I64, P, P]),
+                (L.mmq_mxfp4_experts, INT, [P, P, I64, P, P, I64, P, INT, I64, I64, I64, I64, P]),
+                (L.experts_sort, INT, [P, INT, I64, I64, P, P, P, P, P]),
+                (L.experts_gather, INT, [P, INT, P, P, I64, I64, I64, P]),
+                (L.experts_combine, INT, [P, INT, P, P, P, INT, I64, I64, I64, P]),
+                (L.experts_combine_grad, INT, [P, INT, P, INT, P, P, P, P, I64, I64, I64, P])):
+            f.restype, f.argtypes = res, args
         _lib = L
     return _lib
 
@@ -73,7 +85,9 @@ EXPORTS = ("qpg_strerror", "qpg_q8_1_bytes", "quantize_q8_1", "mmq_q4K", "mmq_q6
            "mmq_q6K_q8", "mmq_q4K_isums", "mmq_q6K_isums", "qpg_q6K_prep_bytes", "q6K_prepare",
            "mmq_q6K_prep_q8", "mmq_q6K_prep_isums", "qpg_q6K_exp_bytes", "q6K_expand", "mmq_q6K_exp_q8",
            "mmq_q6K_exp_csums", "qpg_mmq_sk_bytes", "mmq_q4K_q8_sk", "mmq_q6K_q8_sk", "mmq_q6K_prep_q8_sk",
-           "mmq_q6K_exp_q8_sk", "mmq_q4K_noalloc")
+           "mmq_q6K_exp_q8_sk", "mmq_q4K_noalloc", "qpg_mxfp4_bytes", "quantize_mxfp4", "dequantize_mxfp4",
+           "mmq_mxfp4_mx", "mmq_mxfp4", "qpg_experts_sort_bytes", "experts_sort", "mmq_mxfp4_experts",
+           "experts_gather", "experts_combine", "experts_combine_grad")
 
 
 def _check(rc: int, what: str):
@@ -358,3 +372,290 @@ def mmq_q6K_prep_q8_sk(wp, xq, M, N, K, y=None, ws=None, stream=None):
 
 def mmq_q6K_exp_q8_sk(we, xq, M, N, K, y=None, ws=None, stream=None):
     return _mmq_sk("q6K_exp", we, xq, M, N, K, y, ws, stream)
+
+
+# ---- MXFP4 and experts. The tensors of a call lie on one device, which need not be the current
+# one. Outputs and workspaces that are not given are allocated on the stream the call runs on.
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}      # QPG_F32, QPG_F16, QPG_BF16
+
+
+def _run(t: torch.Tensor, stream, call):
+    """call(raw stream) with t's device current and `stream` (t's device's current one if None)
+    the one that torch allocates on."""
+    if not t.is_cuda:
+        raise QPGError(QPG_EINVAL, "the operands must be device tensors")
+    if stream is None and t.device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    if stream is not None and stream.device != t.device:
+        raise QPGError(QPG_EINVAL, f"the stream is on {stream.device}, the operands on {t.device}")
+    with torch.cuda.device(t.device), torch.cuda.stream(stream):
+        return call(torch.cuda.current_stream().cuda_stream)
+
+
+def _type(dtype, name: str) -> int:
+    if dtype not in _TYPES:
+        raise QPGError(QPG_EINVAL, f"{name} must be float32, float16 or bfloat16, got {dtype}")
+    return _TYPES[dtype]
+
+
+def _float(t: torch.Tensor, name: str, dims: int = 2) -> int:
+    """The type code of a float operand, contiguous and of `dims` dimensions."""
+    code = _type(t.dtype, name)
+    _dev(t, t.dtype, name)
+    if t.dim() != dims:
+        raise QPGError(QPG_EINVAL, f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    return code
+
+
+def _is(t: torch.Tensor, dtype, shape, name: str, ref: torch.Tensor):
+    """An operand of a known type and shape, on ref's device."""
+    _dev(t, dtype, name)
+    _same_device(t, ref, name)
+    if tuple(t.shape) != tuple(shape):
+        raise QPGError(QPG_EINVAL, f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _mx_bytes(rows: int, K: int, name: str) -> int:
+    n = mxfp4_bytes(rows, K)
+    if n == 0:
+        raise QPGError(QPG_EINVAL, f"unsupported MXFP4 shape of {name}: {rows} x {K}")
+    return n
+
+
+def _mx(t: torch.Tensor, rows: int, K: int, name: str, ref: torch.Tensor):
+    """An MXFP4 operand of rows x K values (uint8, at least its size)."""
+    _out(t, torch.uint8, name, _mx_bytes(rows, K, name), ref)
+
+
+def mxfp4_bytes(rows: int, K: int) -> int:
+    """Size of an MXFP4 buffer of rows x K values (0: unsupported shape)."""
+    return int(lib().qpg_mxfp4_bytes(rows, K))
+
+
+def quantize_mxfp4(x: torch.Tensor, xm: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """x [M, K] (float32, float16 or bfloat16) -> uint8 MXFP4 buffer of mxfp4_bytes(M, K) bytes."""
+    code = _float(x, "x")
+    M, K = x.shape
+    nbytes = _mx_bytes(M, K, "x")
+    if xm is not None:
+        _mx(xm, M, K, "xm", x)
+
+    def call(s):
+        out = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if xm is None else xm
+        _check(lib().quantize_mxfp4(x.data_ptr(), code, out.data_ptr(), M, K, s), "quantize_mxfp4")
+        return out
+    return _run(x, stream, call)
+
+
+def dequantize_mxfp4(xm: torch.Tensor, M: int, K: int, y: torch.Tensor | None = None, dtype=torch.float32,
+                     stream=None) -> torch.Tensor:
+    """MXFP4 buffer -> y [M, K], the values its codes stand for (dtype: y's where y is given)."""
+    _mx(xm, M, K, "xm", xm)
+    if y is not None:
+        dtype = y.dtype
+    code = _type(dtype, "y")
+    if y is not None:
+        _is(y, dtype, (M, K), "y", xm)
+
+    def call(s):
+        out = torch.empty((M, K), dtype=dtype, device=xm.device) if y is None else y
+        _check(lib().dequantize_mxfp4(xm.data_ptr(), out.data_ptr(), code, M, K, s), "dequantize_mxfp4")
+        return out
+    return _run(xm, stream, call)
+
+
+def mmq_mxfp4(w: torch.Tensor, x: torch.Tensor, N: int, y=None, xm_ws=None, dtype=torch.float32,
+              stream=None) -> torch.Tensor:
+    """y [M, N] = MXFP4(x [M, K]) x w [N, K]^T from float activations; w is an MXFP4 buffer. xm_ws:
+    mxfp4_bytes(M, K) bytes of workspace that holds MXFP4(x) afterwards."""
+    x_code = _float(x, "x")
+    M, K = x.shape
+    nbytes = _mx_bytes(M, K, "x")
+    _mx(w, N, K, "w", x)
+    if y is not None:
+        dtype = y.dtype
+    y_code = _type(dtype, "y")
+    if y is not None:
+        _is(y, dtype, (M, N), "y", x)
+    if xm_ws is not None:
+        _mx(xm_ws, M, K, "xm_ws", x)
+
+    def call(s):
+        out = torch.empty((M, N), dtype=dtype, device=x.device) if y is None else y
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if xm_ws is None else xm_ws
+        _check(lib().mmq_mxfp4(w.data_ptr(), x.data_ptr(), x_code, out.data_ptr(), y_code, M, N, K, ws.data_ptr(), s),
+               "mmq_mxfp4")
+        return out
+    return _run(x, stream, call)
+
+
+def mmq_mxfp4_mx(w: torch.Tensor, xm: torch.Tensor, M: int, N: int, K: int, y=None, dtype=torch.float32,
+                 stream=None) -> torch.Tensor:
+    """y [M, N] = xm [M, K] x w [N, K]^T, both MXFP4 buffers."""
+    _mx(xm, M, K, "xm", xm)
+    _mx(w, N, K, "w", xm)
+    if y is not None:
+        dtype = y.dtype
+    code = _type(dtype, "y")
+    if y is not None:
+        _is(y, dtype, (M, N), "y", xm)
+
+    def call(s):
+        out = torch.empty((M, N), dtype=dtype, device=xm.device) if y is None else y
+        _check(lib().mmq_mxfp4_mx(w.data_ptr(), xm.data_ptr(), out.data_ptr(), code, M, N, K, s), "mmq_mxfp4_mx")
+        return out
+    return _run(xm, stream, call)
+
+
+def experts_sort(ids: torch.Tensor, E: int, offsets=None, order=None, slots=None, ws=None, stream=None):
+    """ids [T, top_k] (int32 or int64) -> (offsets [E + 1], order [T * top_k], slots [T, top_k]), int32:
+    the choices sorted by expert, stably. A choice outside [0, E) gets no row (slots -1); order
+    is -1 behind the last row."""
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise QPGError(QPG_EINVAL, f"ids must be int32 or int64, got {ids.dtype}")
+    _dev(ids, ids.dtype, "ids")
+    if ids.dim() != 2:
+        raise QPGError(QPG_EINVAL, f"ids must have 2 dimensions, got {tuple(ids.shape)}")
+    S = ids.numel()
+    if S < 1 or not 1 <= E <= 1024:
+        raise QPGError(QPG_EINVAL, f"unsupported sort of {S} choices over {E} experts")
+    for t, shape, name in ((offsets, (E + 1,), "offsets"), (order, (S,), "order"), (slots, ids.shape, "slots")):
+        if t is not None:
+            _is(t, torch.int32, shape, name, ids)
+    nws = int(lib().qpg_experts_sort_bytes(S, E))
+    if ws is not None:
+        _out(ws, torch.uint8, "ws", nws, ids)
+
+    def call(s):
+        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=ids.device)  # noqa: E731
+        o = new(E + 1) if offsets is None else offsets
+        r = new(S) if order is None else order
+        p = new(*ids.shape) if slots is None else slots
+        w = torch.empty(nws, dtype=torch.uint8, device=ids.device) if ws is None and nws else ws
+        _check(lib().experts_sort(ids.data_ptr(), ids.element_size(), S, E, o.data_ptr(), r.data_ptr(), p.data_ptr(),
+                                  None if w is None else w.data_ptr(), s), "experts_sort")
+        return o, r, p
+    return _run(ids, stream, call)
+
+
+def experts_sort_bytes(S: int, E: int) -> int:
+    """Bytes of experts_sort's workspace (0: it needs none)."""
+    return int(lib().qpg_experts_sort_bytes(S, E))
+
+
+def mmq_mxfp4_experts(w: torch.Tensor, xm: torch.Tensor, rows: int, offsets: torch.Tensor, order, top_k: int, E: int,
+                      N: int, K: int, y=None, dtype=torch.float32, stream=None) -> torch.Tensor:
+    """y[p] = activation row x w[expert of p]^T for every sorted row p. w: MXFP4 of E * N rows, xm:
+    MXFP4 of `rows` rows -- the tokens, read through order [S] (row order[p] // top_k), or with
+    order None the rows in sorted order themselves (S = rows). Rows of y behind the last
+    (offsets[E]) are not written."""
+    _mx(xm, rows, K, "xm", xm)
+    _mx(w, E * N, K, "w", xm)
+    _is(offsets, torch.int32, (E + 1,), "offsets", xm)
+    S = rows if order is None else order.numel()
+    if order is not None:
+        _is(order, torch.int32, (S,), "order", xm)
+    if y is not None:
+        dtype = y.dtype
+    code = _type(dtype, "y")
+    if y is not None:
+        _is(y, dtype, (S, N), "y", xm)
+
+    def call(s):
+        out = torch.empty((S, N), dtype=dtype, device=xm.device) if y is None else y
+        _check(lib().mmq_mxfp4_experts(w.data_ptr(), xm.data_ptr(), rows, offsets.data_ptr(),
+                                       None if order is None else order.data_ptr(), top_k, out.data_ptr(), code, S, E, N,
+                                       K, s), "mmq_mxfp4_experts")
+        return out
+    return _run(xm, stream, call)
+
+
+def _slots(slots: torch.Tensor, ref: torch.Tensor):
+    _dev(slots, torch.int32, "slots")
+    _same_device(slots, ref, "slots")
+    if slots.dim() != 2:
+        raise QPGError(QPG_EINVAL, f"slots must have 2 dimensions, got {tuple(slots.shape)}")
+    return slots.shape
+
+
+def experts_gather(x: torch.Tensor, slots: torch.Tensor, xs=None, stream=None) -> torch.Tensor:
+    """xs [T * top_k, H]: row slots[t, j] is x[t]. Rows that no choice has are not
+    written."""
+    code = _float(x, "x")
+    T, top_k = _slots(slots, x)
+    H = x.shape[1]
+    if x.shape[0] != T:
+        raise QPGError(QPG_EINVAL, f"x has {x.shape[0]} tokens, slots {T}")
+    if xs is not None:
+        _is(xs, x.dtype, (T * top_k, H), "xs", x)
+
+    def call(s):
+        out = torch.empty((T * top_k, H), dtype=x.dtype, device=x.device) if xs is None else xs
+        _check(lib().experts_gather(x.data_ptr(), code, slots.data_ptr(), out.data_ptr(), T, top_k, H, s),
+               "experts_gather")
+        return out
+    return _run(x, stream, call)
+
+
+def _combine(ys, slots, weights, y, dtype, stream, what):
+    ys_code = _float(ys, "ys")
+    T, top_k = _slots(slots, ys)
+    H = ys.shape[1]
+    if ys.shape[0] != T * top_k:
+        raise QPGError(QPG_EINVAL, f"{ys.shape[0]} sorted rows, slots for {T * top_k}")
+    if weights is not None:
+        _is(weights, torch.float32, (T, top_k), "weights", ys)
+    if y is not None:
+        dtype = y.dtype
+    elif dtype is None:
+        dtype = ys.dtype
+    y_code = _type(dtype, "y")
+    if y is not None:
+        _is(y, dtype, (T, H), "y", ys)
+
+    def call(s):
+        out = torch.empty((T, H), dtype=dtype, device=ys.device) if y is None else y
+        _check(lib().experts_combine(ys.data_ptr(), ys_code, slots.data_ptr(),
+                                     None if weights is None else weights.data_ptr(), out.data_ptr(), y_code, T, top_k, H,
+                                     s), what)
+        return out
+    return _run(ys, stream, call)
+
+
+def experts_gather_grad(dxs: torch.Tensor, slots: torch.Tensor, dx=None, stream=None) -> torch.Tensor:
+    """Gradient of experts_gather: dx [T, H], dx[t] = sum over j of dxs[slots[t, j]] (of dxs's type)."""
+    return _combine(dxs, slots, None, dx, None, stream, "experts_gather_grad")
+
+
+def experts_combine(ys: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, y=None, dtype=None,
+                    stream=None) -> torch.Tensor:
+    """y [T, H]: y[t] = sum over j of weights[t, j] * ys[slots[t, j]]; choices without a row add nothing.
+    dtype: y's type (ys's if neither is given)."""
+    if weights is None:
+        raise QPGError(QPG_EINVAL, "weights must be a float32 tensor")
+    return _combine(ys, slots, weights, y, dtype, stream, "experts_combine")
+
+
+def experts_combine_grad(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, dys=None,
+                         dweights=None, stream=None):
+    """Gradients of experts_combine: (dys [T * top_k, H] of ys's type, dweights [T, top_k] float32).
+    Rows of dys that no choice has are not written."""
+    dy_code, ys_code = _float(dy, "dy"), _float(ys, "ys")
+    T, top_k = _slots(slots, ys)
+    H = ys.shape[1]
+    _is(dy, dy.dtype, (T, H), "dy", ys)
+    _is(ys, ys.dtype, (T * top_k, H), "ys", ys)
+    _is(weights, torch.float32, (T, top_k), "weights", ys)
+    if dys is not None:
+        _is(dys, ys.dtype, (T * top_k, H), "dys", ys)
+    if dweights is not None:
+        _is(dweights, torch.float32, (T, top_k), "dweights", ys)
+
+    def call(s):
+        d = torch.empty((T * top_k, H), dtype=ys.dtype, device=ys.device) if dys is None else dys
+        dw = torch.empty((T, top_k), dtype=torch.float32, device=ys.device) if dweights is None else dweights
+        _check(lib().experts_combine_grad(dy.data_ptr(), dy_code, ys.data_ptr(), ys_code, slots.data_ptr(),
+                                          weights.data_ptr(), d.data_ptr(), dw.data_ptr(), T, top_k, H, s),
+               "experts_combine_grad")
+        return d, dw
+    return _run(ys, stream, call)

@@ -4,6 +4,7 @@
 
 #include "../../include/qpg.h"
 #include "qpg_common.h"
+#include "qpg_mx.h"
 
 namespace {
 
@@ -217,6 +218,8 @@ int mmq_sk_checked(int form, const void* w, const void* xq, float* y, int64_t M,
 }
 
 }  // namespace
+
+int qpg_check_device() { return check_device(); }
 
 extern "C" {
 

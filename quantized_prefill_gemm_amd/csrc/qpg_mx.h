@@ -1,0 +1,72 @@
+// Internal definitions shared by the MXFP4 and expert kernels of libqpg (not part of the C ABI).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/qpg.h"
+
+namespace qpg {
+
+typedef int int32x2 __attribute__((ext_vector_type(2)));
+typedef int int32x4 __attribute__((ext_vector_type(4)));
+typedef int int32x8 __attribute__((ext_vector_type(8)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+constexpr int MX_BLOCK = 32;          // values that share one scale byte
+
+// Storage type of a QPG_F32 / QPG_F16 / QPG_BF16 argument; conversions from f32 round to
+// nearest even (half a step of the stored type, once, at the end of each operator).
+template <int TYPE> struct Store;
+template <> struct Store<QPG_F32> { typedef float type; };
+template <> struct Store<QPG_F16> { typedef _Float16 type; };
+template <> struct Store<QPG_BF16> { typedef __bf16 type; };
+
+// N values of T moved as one access (16 bytes or less) and widened to f32.
+template <typename T, int N> struct alignas(sizeof(T) * N) Pack { T v[N]; };
+
+// f32 value of a scale byte: 2^(e - 127), NaN for 255. 2^-127 is a subnormal f32.
+__device__ __forceinline__ float mx_scale(int e)
+{
+    return __int_as_float(e == 255 ? 0x7FC00000 : e == 0 ? 0x00400000 : e << 23);
+}
+
+inline size_t type_bytes(int type) { return type == QPG_F32 ? 4 : 2; }
+
+}  // namespace qpg
+
+// QPG_OK on a gfx950 device that is current, else QPG_EDEVICE (api.hip).
+int qpg_check_device();
+
+// Calls F.operator()<TYPE>() for a validated QPG_F32 / QPG_F16 / QPG_BF16 value.
+template <typename F>
+hipError_t qpg_by_type(int type, F f)
+{
+    switch (type) {
+    case QPG_F32: return f(std::integral_constant<int, QPG_F32>());
+    case QPG_F16: return f(std::integral_constant<int, QPG_F16>());
+    case QPG_BF16: return f(std::integral_constant<int, QPG_BF16>());
+    default: return hipErrorInvalidValue;
+    }
+}
+
+// Kernel launchers (arguments validated by the C ABI layer); they return hipGetLastError().
+hipError_t qpg_launch_quantize_mxfp4(const void* x, int x_type, void* xm, int64_t M, int64_t K, hipStream_t s);
+hipError_t qpg_launch_dequantize_mxfp4(const void* xm, void* y, int y_type, int64_t M, int64_t K, hipStream_t s);
+hipError_t qpg_launch_mmq_mxfp4(const void* w, const void* xm, void* y, int y_type, int64_t M, int64_t N, int64_t K,
+                                hipStream_t s);
+hipError_t qpg_launch_mmq_mxfp4_experts(const void* w, const void* xm, int64_t rows, const int32_t* offsets,
+                                        const int32_t* order, int64_t top_k, void* y, int y_type, int64_t S, int64_t E,
+                                        int64_t N, int64_t K, hipStream_t s);
+int qpg_experts_sort_blocks(int64_t S);
+hipError_t qpg_launch_experts_sort(const void* ids, int id_bytes, int64_t S, int64_t E, int32_t* offsets,
+                                   int32_t* order, int32_t* slots, void* ws, hipStream_t s);
+hipError_t qpg_launch_experts_gather(const void* x, int type, const int32_t* slots, void* xs, int64_t T, int64_t top_k,
+                                     int64_t H, hipStream_t s);
+hipError_t qpg_launch_experts_combine(const void* ys, int ys_type, const int32_t* slots, const float* weights, void* y,
+                                      int y_type, int64_t T, int64_t top_k, int64_t H, hipStream_t s);
+hipError_t qpg_launch_experts_combine_grad(const void* dy, int dy_type, const void* ys, int ys_type,
+                                           const int32_t* slots, const float* weights, void* dys, float* dweights,
+                                           int64_t T, int64_t top_k, int64_t H, hipStream_t s);
