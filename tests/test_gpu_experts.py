@@ -166,7 +166,9 @@ def test_gradients_against_differences():
 
 PRODUCTS = [(1, 1, 1, 1, 32, "uniform"), (4, 4, 32, 300, 1056, "uniform"), (3, 2, 8, 17, 96, "drop"),
             (40, 2, 3, 130, 544, "skew"), (64, 1, 4, 64, 512, "one"), (200, 2, 4, 260, 992, "drop"), (9, 3, 5, 50, 64, "none"),
-            (700, 2, 5, 200, 1312, "skew"), (600, 1, 2, 513, 768, "drop"), (100, 4, 200, 48, 160, "uniform")]
+            (700, 2, 5, 200, 1312, "skew"), (600, 1, 2, 513, 768, "drop"), (100, 4, 200, 48, 160, "uniform"),
+            (1500, 1, 4, 1400, 544, "skew"), (3000, 2, 3, 2100, 768, "drop"), (2500, 2, 3, 2500, 640, "skew"),
+            (300, 2, 40, 300, 800, "uniform")]
 
 
 @pytest.mark.parametrize("T,top_k,E,N,K,how", PRODUCTS)
@@ -239,7 +241,8 @@ def layer(ids, x, w, wts, E, N, K, dtype):
     return B.experts_combine(ys, slots, wts, dtype=dtype)
 
 
-@pytest.mark.parametrize("T,top_k,E,N,K,how", [(5, 2, 8, 96, 256, "drop"), (150, 3, 6, 200, 480, "skew")])
+@pytest.mark.parametrize("T,top_k,E,N,K,how", [(5, 2, 8, 96, 256, "drop"), (150, 3, 6, 200, 480, "skew"),
+                                               (400, 2, 4, 700, 1056, "drop")])
 def test_operators_together_and_in_a_graph(T, top_k, E, N, K, how):
     """Sort, quantise, product and weighted sum in one run against 64 bits; on two streams at
     once; captured, and replayed with other routings and activations, eager work in between."""

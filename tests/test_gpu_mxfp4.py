@@ -89,11 +89,13 @@ def product_case(M, N, K, seed, kind="float32", scale=0.02):
     return w, torch.from_numpy(x.astype(np.float32)).to(KINDS[kind])
 
 
-# Every tile form and its edges: rows around 16, 32, 64, 128 and 256, odd widths, K with whole
-# and partial units, one block alone.
+# Every form and its edges: rows around 16, 32, 64, 128 and 256, odd widths, K with whole and
+# partial units, one block alone; one tile to a workgroup, and several (the last four).
 SHAPES = [(1, 1, 32), (1, 4096, 4096), (2, 7, 96), (15, 100, 544), (16, 256, 512), (17, 33, 480), (31, 130, 1024),
           (33, 64, 1056), (48, 1000, 2912), (64, 512, 2048), (65, 129, 64), (100, 260, 992), (127, 384, 768),
-          (129, 255, 1280), (200, 640, 2080), (257, 513, 1312), (512, 256, 256), (300, 1030, 4096), (700, 900, 2912)]
+          (129, 255, 1280), (200, 640, 2080), (257, 513, 1312), (512, 256, 256), (300, 1030, 4096), (700, 900, 2912),
+          (200, 1500, 544), (190, 1600, 640), (200, 1501, 800), (513, 2050, 1024), (600, 2100, 288), (300, 40000, 320),
+          (3000, 3100, 768), (4200, 4200, 544), (2600, 4097, 640)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -124,7 +126,8 @@ def test_product_from_narrow_activations(M, N, K, kind):
     assert (np.abs(f64(y) - exact) <= R.product_bound(xv, wv, exact, "float32")).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 40, 1120), (40, 72, 1120), (200, 300, 1120)])
+@pytest.mark.parametrize("M,N,K", [(3, 40, 1120), (40, 72, 1120), (200, 300, 1120), (250, 1400, 1120), (250, 1400, 896),
+                                   (600, 2100, 1120), (3000, 3100, 640)])
 def test_scales_of_any_size_and_nan(M, N, K):
     """Scale bytes over the whole range a product stays finite in, and NaN scales: a NaN block
     of x makes its row of y NaN, one of w its column, and nothing else."""
@@ -145,7 +148,8 @@ def test_scales_of_any_size_and_nan(M, N, K):
     assert (np.abs(y - exact)[ok] <= bound[ok]).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 37, 160), (70, 131, 1056), (300, 257, 544)])
+@pytest.mark.parametrize("M,N,K", [(5, 37, 160), (70, 131, 1056), (300, 257, 544), (300, 1301, 544), (601, 2100, 544),
+                                   (3001, 3100, 544)])
 def test_nothing_outside_the_outputs_is_written(M, N, K):
     w, x = product_case(M, N, K, 3)
     wd, xd = torch.from_numpy(w).to(DEV), x.to(DEV)
@@ -164,10 +168,10 @@ def test_nothing_outside_the_outputs_is_written(M, N, K):
     assert bool((room[:32] == 5.0).all()) and bool((room[32 + M * K:] == 5.0).all())
 
 
-def test_operand_at_the_end_of_its_buffer():
+@pytest.mark.parametrize("M,N,K", [(21, 50, 1056), (250, 1400, 1056), (250, 1400, 1152), (600, 2100, 1056)])
+def test_operand_at_the_end_of_its_buffer(M, N, K):
     """The last rows' partial units: the result does not depend on what follows the operands
     (scale bytes of NaN right behind both planes)."""
-    M, N, K = 21, 50, 1056
     w, x = product_case(M, N, K, 4)
     wd, xd = torch.from_numpy(w).to(DEV), x.to(DEV)
     y = B.mmq_mxfp4(wd, xd, N)
