@@ -18,5 +18,5 @@ __all__ = ["inputs", "q8_1_bytes", "quantize_q8_1", "mmq_q4K", "mmq_q6K", "mmq_q
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        return globals().setdefault(name, getattr(binding, name))      # looked up here from now on
     raise AttributeError(name)

@@ -7,6 +7,7 @@ library has not been built, the first call raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -376,43 +377,62 @@ def mmq_q6K_exp_q8_sk(we, xq, M, N, K, y=None, ws=None, stream=None):
 
 # ---- MXFP4 and experts. The tensors of a call lie on one device, which need not be the current
 # one. Outputs and workspaces that are not given are allocated on the stream the call runs on.
+# A small call is bound by the host (a launch takes 3.7 us, torch.cuda.current_stream() 2.9, an
+# allocation 1.4), so the checks below are one comparison each where nothing is wrong.
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}      # QPG_F32, QPG_F16, QPG_BF16
+_raw_stream = torch._C._cuda_getCurrentRawStream                      # current_stream().cuda_stream, 0.1 us
 
 
 def _run(t: torch.Tensor, stream, call):
     """call(raw stream) with t's device current and `stream` (t's device's current one if None)
     the one that torch allocates on."""
-    if not t.is_cuda:
-        raise QPGError(QPG_EINVAL, "the operands must be device tensors")
-    if stream is None and t.device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
+    dev = t.get_device()
+    if stream is None and dev == torch.cuda.current_device():
+        return call(_raw_stream(dev))
     if stream is not None and stream.device != t.device:
         raise QPGError(QPG_EINVAL, f"the stream is on {stream.device}, the operands on {t.device}")
-    with torch.cuda.device(t.device), torch.cuda.stream(stream):
-        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return call(_raw_stream(dev))
 
 
 def _type(dtype, name: str) -> int:
-    if dtype not in _TYPES:
+    code = _TYPES.get(dtype)
+    if code is None:
         raise QPGError(QPG_EINVAL, f"{name} must be float32, float16 or bfloat16, got {dtype}")
-    return _TYPES[dtype]
+    return code
 
 
-def _float(t: torch.Tensor, name: str, dims: int = 2) -> int:
-    """The type code of a float operand, contiguous and of `dims` dimensions."""
+def _float(t: torch.Tensor, name: str) -> int:
+    """The type code of a float operand, a contiguous matrix on a device."""
     code = _type(t.dtype, name)
-    _dev(t, t.dtype, name)
-    if t.dim() != dims:
-        raise QPGError(QPG_EINVAL, f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    if t.get_device() < 0 or not t.is_contiguous():
+        _dev(t, t.dtype, name)
+    if t.dim() != 2:
+        raise QPGError(QPG_EINVAL, f"{name} must have 2 dimensions, got {tuple(t.shape)}")
     return code
 
 
 def _is(t: torch.Tensor, dtype, shape, name: str, ref: torch.Tensor):
     """An operand of a known type and shape, on ref's device."""
-    _dev(t, dtype, name)
-    _same_device(t, ref, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.get_device() != ref.get_device() or not t.is_contiguous():
+        _dev(t, dtype, name)
+        _same_device(t, ref, name)
+    if t.shape != shape:
         raise QPGError(QPG_EINVAL, f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _mx(t: torch.Tensor, rows: int, K: int, name: str, ref: torch.Tensor):
+    """An MXFP4 operand of rows x K values (uint8, at least its size)."""
+    need = _mx_bytes(rows, K, name)
+    if t.dtype is not torch.uint8 or t.get_device() != ref.get_device() or t.get_device() < 0 \
+            or not t.is_contiguous() or t.numel() < need:
+        _out(t, torch.uint8, name, need, ref)
+
+
+@functools.lru_cache(maxsize=4096)
+def mxfp4_bytes(rows: int, K: int) -> int:
+    """Size of an MXFP4 buffer of rows x K values (0: unsupported shape)."""
+    return int(lib().qpg_mxfp4_bytes(rows, K))
 
 
 def _mx_bytes(rows: int, K: int, name: str) -> int:
@@ -422,14 +442,13 @@ def _mx_bytes(rows: int, K: int, name: str) -> int:
     return n
 
 
-def _mx(t: torch.Tensor, rows: int, K: int, name: str, ref: torch.Tensor):
-    """An MXFP4 operand of rows x K values (uint8, at least its size)."""
-    _out(t, torch.uint8, name, _mx_bytes(rows, K, name), ref)
-
-
-def mxfp4_bytes(rows: int, K: int) -> int:
-    """Size of an MXFP4 buffer of rows x K values (0: unsupported shape)."""
-    return int(lib().qpg_mxfp4_bytes(rows, K))
+def _given(y, dtype, shape, name: str, ref: torch.Tensor):
+    """(dtype, type code) of an output: y's own where y is given, which then has that shape."""
+    if y is None:
+        return dtype, _type(dtype, name)
+    code = _type(y.dtype, name)
+    _is(y, y.dtype, shape, name, ref)
+    return y.dtype, code
 
 
 def quantize_mxfp4(x: torch.Tensor, xm: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -451,11 +470,7 @@ def dequantize_mxfp4(xm: torch.Tensor, M: int, K: int, y: torch.Tensor | None = 
                      stream=None) -> torch.Tensor:
     """MXFP4 buffer -> y [M, K], the values its codes stand for (dtype: y's where y is given)."""
     _mx(xm, M, K, "xm", xm)
-    if y is not None:
-        dtype = y.dtype
-    code = _type(dtype, "y")
-    if y is not None:
-        _is(y, dtype, (M, K), "y", xm)
+    dtype, code = _given(y, dtype, (M, K), "y", xm)
 
     def call(s):
         out = torch.empty((M, K), dtype=dtype, device=xm.device) if y is None else y
@@ -472,11 +487,7 @@ def mmq_mxfp4(w: torch.Tensor, x: torch.Tensor, N: int, y=None, xm_ws=None, dtyp
     M, K = x.shape
     nbytes = _mx_bytes(M, K, "x")
     _mx(w, N, K, "w", x)
-    if y is not None:
-        dtype = y.dtype
-    y_code = _type(dtype, "y")
-    if y is not None:
-        _is(y, dtype, (M, N), "y", x)
+    dtype, y_code = _given(y, dtype, (M, N), "y", x)
     if xm_ws is not None:
         _mx(xm_ws, M, K, "xm_ws", x)
 
@@ -494,17 +505,19 @@ def mmq_mxfp4_mx(w: torch.Tensor, xm: torch.Tensor, M: int, N: int, K: int, y=No
     """y [M, N] = xm [M, K] x w [N, K]^T, both MXFP4 buffers."""
     _mx(xm, M, K, "xm", xm)
     _mx(w, N, K, "w", xm)
-    if y is not None:
-        dtype = y.dtype
-    code = _type(dtype, "y")
-    if y is not None:
-        _is(y, dtype, (M, N), "y", xm)
+    dtype, code = _given(y, dtype, (M, N), "y", xm)
 
     def call(s):
         out = torch.empty((M, N), dtype=dtype, device=xm.device) if y is None else y
         _check(lib().mmq_mxfp4_mx(w.data_ptr(), xm.data_ptr(), out.data_ptr(), code, M, N, K, s), "mmq_mxfp4_mx")
         return out
     return _run(xm, stream, call)
+
+
+@functools.lru_cache(maxsize=4096)
+def experts_sort_bytes(S: int, E: int) -> int:
+    """Bytes of experts_sort's workspace (0: it needs none, or the shape is not supported)."""
+    return int(lib().qpg_experts_sort_bytes(S, E))
 
 
 def experts_sort(ids: torch.Tensor, E: int, offsets=None, order=None, slots=None, ws=None, stream=None):
@@ -522,25 +535,24 @@ def experts_sort(ids: torch.Tensor, E: int, offsets=None, order=None, slots=None
     for t, shape, name in ((offsets, (E + 1,), "offsets"), (order, (S,), "order"), (slots, ids.shape, "slots")):
         if t is not None:
             _is(t, torch.int32, shape, name, ids)
-    nws = int(lib().qpg_experts_sort_bytes(S, E))
+    nws = experts_sort_bytes(S, E)
     if ws is not None:
         _out(ws, torch.uint8, "ws", nws, ids)
 
     def call(s):
-        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=ids.device)  # noqa: E731
-        o = new(E + 1) if offsets is None else offsets
-        r = new(S) if order is None else order
-        p = new(*ids.shape) if slots is None else slots
-        w = torch.empty(nws, dtype=torch.uint8, device=ids.device) if ws is None and nws else ws
+        o, r, p, w = offsets, order, slots, ws
+        if o is None:
+            o = torch.empty(E + 1, dtype=torch.int32, device=ids.device)
+        if r is None:
+            r = torch.empty(S, dtype=torch.int32, device=ids.device)
+        if p is None:
+            p = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
+        if w is None and nws:
+            w = torch.empty(nws, dtype=torch.uint8, device=ids.device)
         _check(lib().experts_sort(ids.data_ptr(), ids.element_size(), S, E, o.data_ptr(), r.data_ptr(), p.data_ptr(),
                                   None if w is None else w.data_ptr(), s), "experts_sort")
         return o, r, p
     return _run(ids, stream, call)
-
-
-def experts_sort_bytes(S: int, E: int) -> int:
-    """Bytes of experts_sort's workspace (0: it needs none)."""
-    return int(lib().qpg_experts_sort_bytes(S, E))
 
 
 def mmq_mxfp4_experts(w: torch.Tensor, xm: torch.Tensor, rows: int, offsets: torch.Tensor, order, top_k: int, E: int,
@@ -555,11 +567,7 @@ def mmq_mxfp4_experts(w: torch.Tensor, xm: torch.Tensor, rows: int, offsets: tor
     S = rows if order is None else order.numel()
     if order is not None:
         _is(order, torch.int32, (S,), "order", xm)
-    if y is not None:
-        dtype = y.dtype
-    code = _type(dtype, "y")
-    if y is not None:
-        _is(y, dtype, (S, N), "y", xm)
+    dtype, code = _given(y, dtype, (S, N), "y", xm)
 
     def call(s):
         out = torch.empty((S, N), dtype=dtype, device=xm.device) if y is None else y
@@ -571,16 +579,16 @@ def mmq_mxfp4_experts(w: torch.Tensor, xm: torch.Tensor, rows: int, offsets: tor
 
 
 def _slots(slots: torch.Tensor, ref: torch.Tensor):
-    _dev(slots, torch.int32, "slots")
-    _same_device(slots, ref, "slots")
+    if slots.dtype is not torch.int32 or slots.get_device() != ref.get_device() or not slots.is_contiguous():
+        _dev(slots, torch.int32, "slots")
+        _same_device(slots, ref, "slots")
     if slots.dim() != 2:
         raise QPGError(QPG_EINVAL, f"slots must have 2 dimensions, got {tuple(slots.shape)}")
     return slots.shape
 
 
 def experts_gather(x: torch.Tensor, slots: torch.Tensor, xs=None, stream=None) -> torch.Tensor:
-    """xs [T * top_k, H]: row slots[t, j] is x[t]. Rows that no choice has are not
-    written."""
+    """xs [T * top_k, H]: row slots[t, j] is x[t]. Rows that no choice has are not written."""
     code = _float(x, "x")
     T, top_k = _slots(slots, x)
     H = x.shape[1]
@@ -605,13 +613,7 @@ def _combine(ys, slots, weights, y, dtype, stream, what):
         raise QPGError(QPG_EINVAL, f"{ys.shape[0]} sorted rows, slots for {T * top_k}")
     if weights is not None:
         _is(weights, torch.float32, (T, top_k), "weights", ys)
-    if y is not None:
-        dtype = y.dtype
-    elif dtype is None:
-        dtype = ys.dtype
-    y_code = _type(dtype, "y")
-    if y is not None:
-        _is(y, dtype, (T, H), "y", ys)
+    dtype, y_code = _given(y, ys.dtype if dtype is None else dtype, (T, H), "y", ys)
 
     def call(s):
         out = torch.empty((T, H), dtype=dtype, device=ys.device) if y is None else y
