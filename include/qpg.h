@@ -294,7 +294,7 @@ int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int
  * experts_combine_grad: dys[slots[t][j]] = weights[t][j] * dy[t] (of ys's type; other rows left as
  *   they were) and dweights f32 [S], dweights[t][j] = <dy[t], ys[slots[t][j]]>, 0 without a row.
  *   In these three, a slots entry outside [0, S) counts as no row; two slots must not name one
- *   row. H >= 1, H < 2^31; any element alignment; 16-byte aligned rows are faster. Outputs
+ *   row. 1 <= H < 2^28; any element alignment; 16-byte aligned rows are faster. Outputs
  *   must not overlap inputs.
  */
 size_t qpg_experts_sort_bytes(int64_t S, int64_t E);

@@ -151,92 +151,155 @@ hipError_t launch_sort(const ID* ids, int64_t S, int E, int32_t* offsets, int32_
 
 // ---------------------------------------------------------------------------- rows
 
-// A row of H values is cut into segments of 64 lanes * VEC * UNROLL values, one wave each: VEC
-// values per access (16 bytes of the wider type where H and the pointers allow, else 1).
-template <typename T, int VEC>
-__device__ __forceinline__ void load_row(float (&f)[VEC], const T* p)
+// Rows are read and written through buffer descriptors that end with the row: a lane past its
+// end reads zeros and writes nothing, and a slot without a row has an empty one. So there is
+// no branch around an access, and all loads of a wave are under way together (with branches the
+// compiler waits for each: the weighted sum of 268 MB took 84 us). VEC values per access: 16
+// bytes of the wider type where H and the pointers allow, else 1.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void* p, int64_t row, int64_t H, int bytes)
 {
-    const Pack<T, VEC> v = *reinterpret_cast<const Pack<T, VEC>*>(p);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = (float)v.v[i];
+    const char* at = static_cast<const char*>(p) + (row < 0 ? 0 : row * H * bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, row < 0 ? 0 : (int)(H * bytes), 0x00020000);
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_row(__amdgpu_buffer_rsrc_t r, unsigned h)
+{
+    constexpr int BYTES = sizeof(T) * VEC;
+    const int off = (int)(h * (unsigned)sizeof(T));
+    if constexpr (BYTES == 16)
+        return __builtin_bit_cast(Pack<T, VEC>, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    else if constexpr (BYTES == 8)
+        return __builtin_bit_cast(Pack<T, VEC>, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+    else if constexpr (BYTES == 4)
+        return __builtin_bit_cast(Pack<T, VEC>, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    else
+        return __builtin_bit_cast(Pack<T, VEC>, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
 }
 template <typename T, int VEC>
-__device__ __forceinline__ void store_row(T* p, const float (&f)[VEC])
+__device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, unsigned h, const Pack<T, VEC>& v)
 {
-    Pack<T, VEC> v;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v.v[i] = (T)f[i];
-    *reinterpret_cast<Pack<T, VEC>*>(p) = v;
+    constexpr int BYTES = sizeof(T) * VEC;
+    const int off = (int)(h * (unsigned)sizeof(T));
+    if constexpr (BYTES == 16)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uint32x4, v), r, off, 0, 0);
+    else if constexpr (BYTES == 8)
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uint32x2, v), r, off, 0, 0);
+    else if constexpr (BYTES == 4)
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, off, 0, 0);
 }
 
 // A slot's row, or -1 where it has none: a value outside [0, S) is treated as -1, so a wrong
 // array never takes a kernel out of its buffers.
+__device__ __forceinline__ int64_t slot_row_of(int32_t r, int64_t S) { return r >= 0 && r < S ? r : -1; }
 __device__ __forceinline__ int64_t slot_row(const int32_t* slots, int64_t slot, int64_t S)
 {
-    const int32_t r = slots[slot];
-    return r >= 0 && r < S ? r : -1;
+    return slot_row_of(__builtin_amdgcn_readfirstlane(slots[slot]), S);       // the same for the wave
 }
 
-constexpr int ROW_UNROLL = 4;
+// Work of one wave: a segment of a token's row, 64 lanes * VEC * UNROLL values. A workgroup's
+// four waves take neighbouring segments of a token, or where a row has fewer the segments of
+// several tokens (per_block: segments a workgroup takes of a token, 1, 2 or 4).
+struct Item {
+    int64_t t;
+    int64_t seg;
+};
+__device__ __forceinline__ Item wave_item(int per_block)
+{
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int shift = per_block >> 1;                 // log2 of 1, 2, 4
+    return {(int64_t)blockIdx.x * (4 >> shift) + (wave >> shift), (int64_t)blockIdx.y * per_block + (wave & (per_block - 1))};
+}
+
+struct Grid {
+    dim3 blocks;
+    int per_block;
+};
+inline Grid grid_of(int64_t tokens, int64_t H, int segment)
+{
+    const int64_t segs = (H + segment - 1) / segment;
+    const int per = segs >= 3 ? 4 : (int)segs;
+    const int64_t y = (segs + per - 1) / per;
+    return {dim3((unsigned)((tokens * per + 3) / 4), (unsigned)(y < 65535 ? y : 65535)), per};
+}
+
+constexpr int GATHER_UNROLL = 4;
 
 // xs[slots[t][j]] = x[t]: a wave reads its segment of a token once and writes it top_k times.
 // T here is only a width: the values are moved, not read.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) gather_kernel(const T* __restrict__ x, const int32_t* __restrict__ slots,
                                                      T* __restrict__ xs, int64_t tokens, int top_k, int64_t H,
-                                                     int segs)
+                                                     int per_block)
 {
-    typedef Pack<T, VEC> P;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t t = item / segs;
-    if (t >= tokens) return;
-    const int64_t h0 = (item - t * segs) * (64 * VEC * ROW_UNROLL) + (threadIdx.x & 63) * VEC;
-    P v[ROW_UNROLL];
+    constexpr int SEG = 64 * VEC * GATHER_UNROLL;
+    const Item it = wave_item(per_block);
+    if (it.t >= tokens) return;
+    const __amdgpu_buffer_rsrc_t from = row_of(x, it.t, H, sizeof(T));
+    for (int64_t s0 = it.seg * SEG; s0 < H; s0 += (int64_t)gridDim.y * per_block * SEG) {
+        const unsigned h0 = (unsigned)s0 + (threadIdx.x & 63) * VEC;
+        Pack<T, VEC> v[GATHER_UNROLL];
 #pragma unroll
-    for (int u = 0; u < ROW_UNROLL; ++u)
-        if (h0 + u * 64 * VEC < H) v[u] = *reinterpret_cast<const P*>(x + t * H + h0 + u * 64 * VEC);
-    for (int j = 0; j < top_k; ++j) {
-        const int64_t row = slot_row(slots, t * top_k + j, tokens * top_k);
-        if (row < 0) continue;
+        for (int u = 0; u < GATHER_UNROLL; ++u) v[u] = load_row<T, VEC>(from, h0 + u * 64 * VEC);
+        for (int j = 0; j < top_k; ++j) {
+            const int64_t row = slot_row(slots, it.t * top_k + j, tokens * top_k);
+            const __amdgpu_buffer_rsrc_t to = row_of(xs, row, H, sizeof(T));
 #pragma unroll
-        for (int u = 0; u < ROW_UNROLL; ++u)
-            if (h0 + u * 64 * VEC < H) *reinterpret_cast<P*>(xs + row * H + h0 + u * 64 * VEC) = v[u];
+            for (int u = 0; u < GATHER_UNROLL; ++u) store_row<T, VEC>(to, h0 + u * 64 * VEC, v[u]);
+        }
     }
 }
 
 // y[t] = sum over j of weights[t][j] * ys[slots[t][j]], in f32, j upwards; weights null: ones
-// (the gradient of the gather).
+// (the gradient of the gather). The rows of four choices are loaded before the first is added.
+constexpr int COMBINE_UNROLL = 2, COMBINE_SLOTS = 4;
+
 template <typename TI, typename TO, int VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const TI* __restrict__ ys, const int32_t* __restrict__ slots,
                                                       const float* __restrict__ weights, TO* __restrict__ y,
-                                                      int64_t tokens, int top_k, int64_t H, int segs)
+                                                      int64_t tokens, int top_k, int64_t H, int per_block)
 {
-    constexpr int U = 2;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t t = item / segs;
-    if (t >= tokens) return;
-    const int64_t h0 = (item - t * segs) * (64 * VEC * U) + (threadIdx.x & 63) * VEC;
-    float acc[U][VEC];
+    constexpr int U = COMBINE_UNROLL, J = COMBINE_SLOTS, SEG = 64 * VEC * U;
+    const Item it = wave_item(per_block);
+    if (it.t >= tokens) return;
+    const __amdgpu_buffer_rsrc_t to = row_of(y, it.t, H, sizeof(TO));
+    for (int64_t s0 = it.seg * SEG; s0 < H; s0 += (int64_t)gridDim.y * per_block * SEG) {
+        const unsigned h0 = (unsigned)s0 + (threadIdx.x & 63) * VEC;
+        float acc[U][VEC];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[u][i] = 0.f;
-    for (int j = 0; j < top_k; ++j) {
-        const int64_t row = slot_row(slots, t * top_k + j, tokens * top_k);
-        if (row < 0) continue;
-        const float w = weights ? weights[t * top_k + j] : 1.f;
+            for (int i = 0; i < VEC; ++i) acc[u][i] = 0.f;
+        for (int j0 = 0; j0 < top_k; j0 += J) {
+            float w[J];
+            Pack<TI, VEC> v[J][U];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const bool on = j0 + j < top_k;
+                const int64_t slot = it.t * top_k + (on ? j0 + j : 0);
+                const int64_t row = on ? slot_row(slots, slot, tokens * top_k) : -1;
+                w[j] = row < 0 ? 0.f : weights ? weights[slot] : 1.f;
+                const __amdgpu_buffer_rsrc_t from = row_of(ys, row, H, sizeof(TI));
+#pragma unroll
+                for (int u = 0; u < U; ++u) v[j][u] = load_row<TI, VEC>(from, h0 + u * 64 * VEC);
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) acc[u][i] += w[j] * (float)v[j][u].v[i];
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (h0 + u * 64 * VEC >= H) continue;
-            float f[VEC];
-            load_row<TI, VEC>(f, ys + row * H + h0 + u * 64 * VEC);
+            Pack<TO, VEC> o;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[u][i] += w * f[i];
+            for (int i = 0; i < VEC; ++i) o.v[i] = (TO)acc[u][i];
+            store_row<TO, VEC>(to, h0 + u * 64 * VEC, o);
         }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (h0 + u * 64 * VEC < H) store_row<TO, VEC>(y + t * H + h0 + u * 64 * VEC, acc[u]);
 }
 
 __device__ __forceinline__ float wave_sum64(float v)
@@ -261,29 +324,36 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const TO* __restrict_
     __shared__ float part[4][GRAD_SLOTS];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const __amdgpu_buffer_rsrc_t dy_row = row_of(dy, t, H, sizeof(TO));
     for (int j0 = 0; j0 < top_k; j0 += GRAD_SLOTS) {
-        int64_t row[GRAD_SLOTS];
+        __amdgpu_buffer_rsrc_t from[GRAD_SLOTS], to[GRAD_SLOTS];
         float w[GRAD_SLOTS], dot[GRAD_SLOTS];
 #pragma unroll
         for (int j = 0; j < GRAD_SLOTS; ++j) {
-            row[j] = j0 + j < top_k ? slot_row(slots, t * top_k + j0 + j, tokens * top_k) : -1;
-            w[j] = j0 + j < top_k ? weights[t * top_k + j0 + j] : 0.f;
+            const bool on = j0 + j < top_k;
+            const int64_t slot = t * top_k + (on ? j0 + j : 0);
+            const int64_t row = on ? slot_row(slots, slot, tokens * top_k) : -1;
+            from[j] = row_of(ys, row, H, sizeof(TI));
+            to[j] = row_of(dys, row, H, sizeof(TI));
+            w[j] = weights[slot];
             dot[j] = 0.f;
         }
-        for (int64_t h = threadIdx.x * VEC; h < H; h += 256 * VEC) {
-            float g[VEC];
-            load_row<TO, VEC>(g, dy + t * H + h);
+        for (int64_t s0 = 0; s0 < H; s0 += 256 * VEC) {
+            const unsigned h = (unsigned)s0 + threadIdx.x * VEC;
+            const Pack<TO, VEC> g = load_row<TO, VEC>(dy_row, h);
+            Pack<TI, VEC> v[GRAD_SLOTS];
+#pragma unroll
+            for (int j = 0; j < GRAD_SLOTS; ++j) v[j] = load_row<TI, VEC>(from[j], h);
 #pragma unroll
             for (int j = 0; j < GRAD_SLOTS; ++j) {
-                if (row[j] < 0) continue;
-                float f[VEC], o[VEC];
-                load_row<TI, VEC>(f, ys + row[j] * H + h);
+                Pack<TI, VEC> o;
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    dot[j] += g[i] * f[i];
-                    o[i] = w[j] * g[i];
+                    // past the row's end g is 0 too, and a slot without a row is not written out
+                    dot[j] += (float)g.v[i] * (float)v[j].v[i];
+                    o.v[i] = (TI)(w[j] * (float)g.v[i]);
                 }
-                store_row<TI, VEC>(dys + row[j] * H + h, o);
+                store_row<TI, VEC>(to[j], h, o);
             }
         }
 #pragma unroll
@@ -294,7 +364,8 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const TO* __restrict_
         __syncthreads();
         if (threadIdx.x < GRAD_SLOTS && j0 + (int)threadIdx.x < top_k) {
             const int j = threadIdx.x;
-            dweights[t * top_k + j0 + j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
+            const bool on = slot_row_of(slots[t * top_k + j0 + j], tokens * top_k) >= 0;
+            dweights[t * top_k + j0 + j] = on ? (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]) : 0.f;
         }
         __syncthreads();
     }
@@ -334,9 +405,9 @@ hipError_t qpg_launch_experts_gather(const void* x, int type, const int32_t* slo
         typedef decltype(unit) U;
         constexpr int VEC = decltype(vec)::value;
         const int64_t n = H * (int64_t)qpg::type_bytes(type) / (int64_t)sizeof(U);
-        const int segs = (int)((n + 64 * VEC * qpg::ROW_UNROLL - 1) / (64 * VEC * qpg::ROW_UNROLL));
-        hipLaunchKernelGGL((qpg::gather_kernel<U, VEC>), dim3((unsigned)((T * segs + 3) / 4)), dim3(256), 0, s,
-                           static_cast<const U*>(x), slots, static_cast<U*>(xs), T, (int)top_k, n, segs);
+        const qpg::Grid g = qpg::grid_of(T, n, 64 * VEC * qpg::GATHER_UNROLL);
+        hipLaunchKernelGGL((qpg::gather_kernel<U, VEC>), g.blocks, dim3(256), 0, s, static_cast<const U*>(x), slots,
+                           static_cast<U*>(xs), T, (int)top_k, n, g.per_block);
         return hipGetLastError();
     };
     const int64_t row = H * (int64_t)qpg::type_bytes(type);
@@ -353,10 +424,10 @@ hipError_t qpg_launch_experts_combine(const void* ys, int ys_type, const int32_t
         typedef typename qpg::Store<decltype(to)::value>::type TO;
         auto go = [&](auto vec) {
             constexpr int VEC = decltype(vec)::value;
-            const int segs = (int)((H + 64 * VEC * 2 - 1) / (64 * VEC * 2));
-            hipLaunchKernelGGL((qpg::combine_kernel<TI, TO, VEC>), dim3((unsigned)((T * segs + 3) / 4)), dim3(256), 0,
-                               s, static_cast<const TI*>(ys), slots, weights, static_cast<TO*>(y), T, (int)top_k, H,
-                               segs);
+            const qpg::Grid g = qpg::grid_of(T, H, 64 * VEC * qpg::COMBINE_UNROLL);
+            hipLaunchKernelGGL((qpg::combine_kernel<TI, TO, VEC>), g.blocks, dim3(256), 0, s,
+                               static_cast<const TI*>(ys), slots, weights, static_cast<TO*>(y), T, (int)top_k, H,
+                               g.per_block);
             return hipGetLastError();
         };
         constexpr int V = 16 / (sizeof(TI) > sizeof(TO) ? sizeof(TI) : sizeof(TO));

@@ -9,6 +9,8 @@
 namespace qpg {
 
 typedef int int32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned uint32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned uint32x4 __attribute__((ext_vector_type(4)));
 typedef int int32x4 __attribute__((ext_vector_type(4)));
 typedef int int32x8 __attribute__((ext_vector_type(8)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
