@@ -176,19 +176,24 @@ __device__ __forceinline__ Pack<T, VEC> load_row(__amdgpu_buffer_rsrc_t r, unsig
     else
         return __builtin_bit_cast(Pack<T, VEC>, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
 }
+// Stores are non-temporal: the rows are not read again here, and ordinary ones push the rows
+// being read out of the caches (gather and gradient, 8192 x 4 rows of 8 KB: 158 -> 138 us; weighted
+// sum and gradients, 4096 x 8: 177 -> 149 us. Non-temporal loads as well: 135 and 161 us).
+constexpr int NONTEMPORAL = 2;
+
 template <typename T, int VEC>
 __device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, unsigned h, const Pack<T, VEC>& v)
 {
     constexpr int BYTES = sizeof(T) * VEC;
     const int off = (int)(h * (unsigned)sizeof(T));
     if constexpr (BYTES == 16)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uint32x4, v), r, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uint32x4, v), r, off, 0, NONTEMPORAL);
     else if constexpr (BYTES == 8)
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uint32x2, v), r, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uint32x2, v), r, off, 0, NONTEMPORAL);
     else if constexpr (BYTES == 4)
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, NONTEMPORAL);
     else
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, off, 0, NONTEMPORAL);
 }
 
 // A slot's row, or -1 where it has none: a value outside [0, S) is treated as -1, so a wrong
