@@ -74,9 +74,11 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place_kernel(const ID* __re
     int before = 0, all = 0;
     if (tid < E) {
         if (gridDim.x == 1) {
+#pragma unroll
             for (int v = 0; v < SORT_WAVES; ++v) all += at[v * E + tid];
         } else {
-            for (unsigned b = 0; b < gridDim.x; ++b) {
+#pragma unroll 16
+            for (unsigned b = 0; b < gridDim.x; ++b) {       // 16 loads under way
                 const int c = counts[(int64_t)b * E + tid];
                 all += c;
                 before += b < blockIdx.x ? c : 0;
@@ -386,12 +388,15 @@ hipError_t by_types(int a, int b, F f)
 
 }  // namespace qpg
 
-// Blocks of the sort: one up to 8192 slots (a single launch), then one per 4096, at most 64.
+// Blocks of the sort: one up to 4096 slots (a single launch, 7.3 us; 16 blocks 6.3), beyond 16,
+// doubled while a block has more than 1024 slots, at most 128 (each reads all blocks' counts).
+// With 128 experts: 8192 slots 6.5 us (one block 11.5), 32768 7.2 us (8 blocks 11.9), 2^20 18.5 us.
 int qpg_experts_sort_blocks(int64_t S)
 {
-    if (S <= 8192) return 1;
-    const int64_t b = (S + 4095) / 4096;
-    return (int)(b < 64 ? b : 64);
+    if (S <= 4096) return 1;
+    int b = 16;
+    while (b < 128 && S > 1024 * (int64_t)b) b *= 2;
+    return b;
 }
 
 hipError_t qpg_launch_experts_sort(const void* ids, int id_bytes, int64_t S, int64_t E, int32_t* offsets,
