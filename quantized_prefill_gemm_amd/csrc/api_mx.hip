@@ -85,6 +85,11 @@ int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int
     if (!aligned(w, 16) || !aligned(x, 16) || !aligned(xm_ws, 16) || !aligned(y, qpg::type_bytes(y_type)))
         return QPG_EALIGN;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (qpg_mmq_mxfp4_fuses(M, N, K)) {
+        const int dv = qpg_check_device();
+        if (dv != QPG_OK) return dv;
+        return status_of(qpg_launch_mmq_mxfp4_fused(w, x, x_type, xm_ws, y, y_type, M, N, K, s));
+    }
     const int rc = quantize(x, x_type, xm_ws, M, K, s);
     if (rc != QPG_OK) return rc;
     return product(w, xm_ws, y, y_type, M, N, K, s);

@@ -18,36 +18,6 @@
 
 namespace qpg {
 
-__device__ __forceinline__ uint32_t quad_max(uint32_t v)
-{
-    uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);   // lane ^ 1
-    v = v > o ? v : o;
-    o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);            // lane ^ 2
-    return v > o ? v : o;
-}
-
-// Eight values of one lane (four lanes a block) to eight codes; e: the block's scale byte.
-__device__ __forceinline__ uint32_t mx_encode8(const float (&f)[8], int& e)
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t a = __float_as_uint(f[i]) & 0x7FFFFFFFu;     // NaN > infinity > finite
-        m = m > a ? m : a;
-    }
-    m = quad_max(m);
-    const bool finite = m < 0x7F800000u;
-    const int field = (int)(m >> 23) - 2;
-    e = finite ? (field > 0 ? field : 0) : 255;
-    const float scale = mx_scale(finite ? e : 127);
-    uint32_t c = 0;
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[0], f[1], scale, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[2], f[3], scale, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[4], f[5], scale, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[6], f[7], scale, 3);
-    return finite ? c : 0u;
-}
-
 constexpr int MX_SLICES = 2;      // 8-value groups per lane, 256 groups apart: more bytes in flight
 
 template <int TYPE>
