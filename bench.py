@@ -12,6 +12,8 @@ Other modes:
   --shards                   the N/8 shares of the 7B layer GEMMs, plain vs K-split entry
                              points (one JSON line per shape)
   --msweep                   the 7B layer GEMM shapes at M = 16 .. 2048 tokens, likewise
+  --experts                  the 7B-shaped stack with 8 MXFP4 experts, two to a token, for its FFN
+                             (one JSON line)
   --q6forms                  the raw, prepared and expanded q6_K forms on the v and down
                              shapes at M = 16 .. 1024, likewise
 For rocprofv3 runs:
@@ -472,6 +474,58 @@ def run_shards(steps: int, warmup: int, shapes=None):
                           "host_bound": bool(host_bound)}), flush=True)
 
 
+def run_experts(steps: int, warmup: int, layers: int = 4, M: int = 1024, E: int = 8, top_k: int = 2):
+    """The stack with experts (random weights and routing) as one HIP graph per pass, and the
+    FFN's operators of one layer alone, eagerly: HIP events around `steps` passes, five rounds,
+    medians. MXFP4 peak: 10.1 PFLOP/s dense."""
+    import statistics
+    import torch
+    from quantized_prefill_gemm_amd import binding as B
+    from quantized_prefill_gemm_amd import inputs
+    from quantized_prefill_gemm_amd.stack import ExpertStack
+    dev = torch.device("cuda:0")
+    gen = torch.Generator(device=dev).manual_seed(inputs.BASE_SEED + 6)
+
+    def mxfp4(rows, K):
+        w = torch.randint(0, 256, (B.mxfp4_bytes(rows, K),), dtype=torch.uint8, device=dev, generator=gen)
+        w[rows * K // 2:] = torch.randint(116, 122, (rows * K // 32,), device=dev, generator=gen).to(torch.uint8)
+        return w
+    weights = [[torch.from_numpy(inputs.make_stack_matrix(layer, idx)[4].reshape(-1)).to(dev) for idx in range(4)]
+               for layer in range(layers)]
+    experts = [[mxfp4(E * N, K) for _, _, N, K in inputs.STACK_LAYER[4:]] for _ in range(layers)]
+    st = ExpertStack(weights, experts, M, E, top_k)
+    for src in (0, 3, 4, 6):
+        st.set_input(0, src, torch.randn(st.x[0][src].shape, device=dev, generator=gen))
+    score, ids = torch.topk(torch.randn((M, E), device=dev, generator=gen), top_k, dim=1)
+    st.set_routing(0, ids, torch.softmax(score, dim=1))
+    graph = st.capture("shared")
+
+    def timed(fn):
+        for _ in range(warmup):
+            fn()
+        t = []
+        for _ in range(ROUNDS):
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            e0.record()
+            for _ in range(steps):
+                fn()
+            e1.record()
+            torch.cuda.synchronize()
+            t.append(e0.elapsed_time(e1) / steps)
+        return statistics.median(t)
+    ms = timed(graph.replay)
+    one = {"experts_sort": lambda: B.experts_sort(st.ids[0], E, st.offsets[0], st.order[0], st.slots[0], st.sort_ws[0]),
+           "quantize_mxfp4": lambda: B.quantize_mxfp4(st.x[0][4], st.xm[0][4]),
+           "gate": lambda: st._experts(0, 4, None), "down_and_combine": lambda: st._experts(0, 6, None)}
+    us = {name: timed(fn) * 1e3 for name, fn in one.items()}
+    gate = 2 * st.S * inputs.STACK_LAYER[4][2] * inputs.STACK_LAYER[4][3]
+    print(json.dumps({"workload": f"{layers}-layer 7B-shaped stack, M={M}, FFN of {E} MXFP4 experts, {top_k} to a token",
+                      "ms_per_pass": round(ms, 4), "tmacs": round(st.macs() / (ms * 1e-3) / 1e12, 1),
+                      "layer_us": {k: round(v, 2) for k, v in us.items()},
+                      "gate_tflops": round(gate / us["gate"] / 1e6, 1), "data": "synthetic"}), flush=True)
+
+
 def copy_calibration(nbytes: int, launches: int):
     import torch
     a = torch.empty(nbytes, dtype=torch.uint8, device="cuda:0").fill_(1)
@@ -504,6 +558,8 @@ def main():
                     help="time the N/8 shares of the 7B layer GEMMs: plain vs K-split entry points")
     ap.add_argument("--msweep", action="store_true",
                     help="time the 7B layer GEMM shapes over M = 16..2048 tokens: plain vs K-split entry points")
+    ap.add_argument("--experts", action="store_true",
+                    help="time the stack with MXFP4 experts for its FFN")
     ap.add_argument("--q6forms", action="store_true",
                     help="time the three q6_K weight forms on the v and down shapes over M = 16..1024")
     a = ap.parse_args()
@@ -516,6 +572,10 @@ def main():
         return
     if a.profile:
         profile_mode(a.profile, a.launches)
+        return
+    if a.experts:
+        run_experts(a.steps if a.steps != ap.get_default("steps") else 20,
+                    a.warmup if a.warmup != ap.get_default("warmup") else 3)
         return
     if a.shards or a.msweep or a.q6forms:
         if a.shards:
