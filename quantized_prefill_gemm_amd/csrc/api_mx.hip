@@ -6,13 +6,18 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxK = (int64_t)1 << 24;
-constexpr int64_t kMaxValues = (int64_t)1 << 40;     // keeps every launch's grid below 2^31 workgroups
+constexpr int64_t kMaxValues = (int64_t)1 << 35;     // an 8-value thread each: a launch holds < 2^32 threads
+constexpr int64_t kMaxTokens = (int64_t)1 << 24;     // likewise, 256 threads to a token
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxRow = (int64_t)1 << 28;        // a row's bytes stay below 2^31
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 bool type_ok(int t) { return t == QPG_F32 || t == QPG_F16 || t == QPG_BF16; }
-int status_of(hipError_t e) { return e == hipSuccess ? QPG_OK : QPG_EHIP; }
+// hipErrorInvalidConfiguration: the launcher's own refusal of more threads than a launch holds.
+int status_of(hipError_t e)
+{
+    return e == hipSuccess ? QPG_OK : e == hipErrorInvalidConfiguration ? QPG_EINVAL : QPG_EHIP;
+}
 
 bool mx_shape_ok(int64_t rows, int64_t K)
 {
@@ -26,7 +31,8 @@ bool product_shape_ok(int64_t M, int64_t N, int64_t K)
 
 bool slots_ok(int64_t T, int64_t top_k, int64_t H)
 {
-    if (T < 1 || top_k < 1 || H < 1 || T >= kMaxDim || top_k >= kMaxDim || H >= kMaxRow) return false;
+    if (T < 1 || top_k < 1 || H < 1 || T >= kMaxTokens || top_k >= kMaxDim || H >= kMaxRow) return false;
+    // the vector lanes of all rows, and a row's segments at one value to a lane
     return T <= (kMaxDim - 1) / top_k && T <= (kMaxValues - 1) / H;
 }
 

@@ -200,10 +200,10 @@ __device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, unsigned h, 
 
 // A slot's row, or -1 where it has none: a value outside [0, S) is treated as -1, so a wrong
 // array never takes a kernel out of its buffers.
-__device__ __forceinline__ int64_t slot_row_of(int32_t r, int64_t S) { return r >= 0 && r < S ? r : -1; }
-__device__ __forceinline__ int64_t slot_row(const int32_t* slots, int64_t slot, int64_t S)
+__device__ __forceinline__ int64_t slot_row(int32_t r, int64_t S)
 {
-    return slot_row_of(__builtin_amdgcn_readfirstlane(slots[slot]), S);       // the same for the wave
+    r = __builtin_amdgcn_readfirstlane(r);             // the same for the wave
+    return r >= 0 && r < S ? r : -1;
 }
 
 // Work of one wave: a segment of a token's row, 64 lanes * VEC * UNROLL values. A workgroup's
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const T* __restrict__ x, co
 #pragma unroll
         for (int u = 0; u < GATHER_UNROLL; ++u) v[u] = load_row<T, VEC>(from, h0 + u * 64 * VEC);
         for (int j = 0; j < top_k; ++j) {
-            const int64_t row = slot_row(slots, it.t * top_k + j, tokens * top_k);
+            const int64_t row = slot_row(slots[it.t * top_k + j], tokens * top_k);
             const __amdgpu_buffer_rsrc_t to = row_of(xs, row, H, sizeof(T));
 #pragma unroll
             for (int u = 0; u < GATHER_UNROLL; ++u) store_row<T, VEC>(to, h0 + u * 64 * VEC, v[u]);
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const T* __restrict__ x, co
 // (the gradient of the gather). The rows of four choices are loaded before the first is added.
 constexpr int COMBINE_UNROLL = 2, COMBINE_SLOTS = 4;
 
-template <typename TI, typename TO, int VEC>
+template <typename TI, typename TO, int VEC, bool WEIGHTED>
 __global__ void __launch_bounds__(256) combine_kernel(const TI* __restrict__ ys, const int32_t* __restrict__ slots,
                                                       const float* __restrict__ weights, TO* __restrict__ y,
                                                       int64_t tokens, int top_k, int64_t H, int per_block)
@@ -280,18 +280,24 @@ __global__ void __launch_bounds__(256) combine_kernel(const TI* __restrict__ ys,
 #pragma unroll
             for (int i = 0; i < VEC; ++i) acc[u][i] = 0.f;
         for (int j0 = 0; j0 < top_k; j0 += J) {
+            int32_t r[J];
             float w[J];
             Pack<TI, VEC> v[J][U];
 #pragma unroll
+            for (int j = 0; j < J; ++j) {                  // a choice past the last: the last again
+                const int64_t slot = it.t * top_k + min(j0 + j, top_k - 1);
+                r[j] = slots[slot];
+                w[j] = WEIGHTED ? weights[slot] : 1.f;
+            }
+#pragma unroll
             for (int j = 0; j < J; ++j) {
-                const bool on = j0 + j < top_k;
-                const int64_t slot = it.t * top_k + (on ? j0 + j : 0);
-                const int64_t row = on ? slot_row(slots, slot, tokens * top_k) : -1;
-                w[j] = row < 0 ? 0.f : weights ? weights[slot] : 1.f;
+                const int64_t row = j0 + j < top_k ? slot_row(r[j], tokens * top_k) : -1;
+                w[j] = row < 0 ? 0.f : w[j];
                 const __amdgpu_buffer_rsrc_t from = row_of(ys, row, H, sizeof(TI));
 #pragma unroll
                 for (int u = 0; u < U; ++u) v[j][u] = load_row<TI, VEC>(from, h0 + u * 64 * VEC);
             }
+            __builtin_amdgcn_sched_barrier(0);             // all loads before the first use
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -334,16 +340,20 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const TO* __restrict_
     const __amdgpu_buffer_rsrc_t dy_row = row_of(dy, t, H, sizeof(TO));
     for (int j0 = 0; j0 < top_k; j0 += GRAD_SLOTS) {
         __amdgpu_buffer_rsrc_t from[GRAD_SLOTS], to[GRAD_SLOTS];
+        int32_t r[GRAD_SLOTS];
         float w[GRAD_SLOTS], dot[GRAD_SLOTS];
 #pragma unroll
         for (int j = 0; j < GRAD_SLOTS; ++j) {
-            const bool on = j0 + j < top_k;
-            const int64_t slot = t * top_k + (on ? j0 + j : 0);
-            const int64_t row = on ? slot_row(slots, slot, tokens * top_k) : -1;
-            from[j] = row_of(ys, row, H, sizeof(TI));
-            to[j] = row_of(dys, row, H, sizeof(TI));
+            const int64_t slot = t * top_k + min(j0 + j, top_k - 1);      // past the last: the last again
+            r[j] = slots[slot];
             w[j] = weights[slot];
             dot[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < GRAD_SLOTS; ++j) {
+            const int64_t row = j0 + j < top_k ? slot_row(r[j], tokens * top_k) : -1;
+            from[j] = row_of(ys, row, H, sizeof(TI));
+            to[j] = row_of(dys, row, H, sizeof(TI));
         }
         for (int64_t s0 = 0; s0 < H; s0 += 256 * VEC) {
             const unsigned h = (unsigned)s0 + threadIdx.x * VEC;
@@ -351,6 +361,7 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const TO* __restrict_
             Pack<TI, VEC> v[GRAD_SLOTS];
 #pragma unroll
             for (int j = 0; j < GRAD_SLOTS; ++j) v[j] = load_row<TI, VEC>(from[j], h);
+            __builtin_amdgcn_sched_barrier(0);             // all loads before the first use
 #pragma unroll
             for (int j = 0; j < GRAD_SLOTS; ++j) {
                 Pack<TI, VEC> o;
@@ -371,8 +382,8 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const TO* __restrict_
         __syncthreads();
         if (threadIdx.x < GRAD_SLOTS && j0 + (int)threadIdx.x < top_k) {
             const int j = threadIdx.x;
-            const bool on = slot_row_of(slots[t * top_k + j0 + j], tokens * top_k) >= 0;
-            dweights[t * top_k + j0 + j] = on ? (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]) : 0.f;
+            const int32_t row = slots[t * top_k + j0 + j];
+            dweights[t * top_k + j0 + j] = row >= 0 && row < tokens * top_k ? (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]) : 0.f;
         }
         __syncthreads();
     }
@@ -435,9 +446,9 @@ hipError_t qpg_launch_experts_combine(const void* ys, int ys_type, const int32_t
         auto go = [&](auto vec) {
             constexpr int VEC = decltype(vec)::value;
             const qpg::Grid g = qpg::grid_of(T, H, 64 * VEC * qpg::COMBINE_UNROLL);
-            hipLaunchKernelGGL((qpg::combine_kernel<TI, TO, VEC>), g.blocks, dim3(256), 0, s,
-                               static_cast<const TI*>(ys), slots, weights, static_cast<TO*>(y), T, (int)top_k, H,
-                               g.per_block);
+            auto kernel = weights ? qpg::combine_kernel<TI, TO, VEC, true> : qpg::combine_kernel<TI, TO, VEC, false>;
+            hipLaunchKernelGGL(kernel, g.blocks, dim3(256), 0, s, static_cast<const TI*>(ys), slots, weights,
+                               static_cast<TO*>(y), T, (int)top_k, H, g.per_block);
             return hipGetLastError();
         };
         constexpr int V = 16 / (sizeof(TI) > sizeof(TO) ? sizeof(TI) : sizeof(TO));
