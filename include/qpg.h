@@ -271,7 +271,7 @@ int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int
 
 /*
  * Experts: T tokens, top_k choices each; slot t*top_k + j is token t's j-th choice. S = T*top_k
- * slots, 1 <= S < 2^31, 1 <= E <= 1024 experts.
+ * slots, 1 <= S <= 2^30, 1 <= E <= 1024 experts. Outputs must not overlap inputs.
  *
  * experts_sort: ids [S] (int32 or int64: id_bytes 4 or 8) -> the slots sorted by expert, stable.
  *   offsets int32 [E + 1]: rows [offsets[e], offsets[e + 1]) of the sorted order are expert e's;
@@ -283,10 +283,10 @@ int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int
  *
  * mmq_mxfp4_experts: y [S][N]; for each row p < offsets[E], of expert e,
  *   y[p] = xm[order[p] / top_k] x w[e]^T, or xm[p] x w[e]^T with order null (activations already
- *   in sorted order; then rows == S). w: MXFP4 of E*N rows, xm: MXFP4 of `rows` rows. Rows of
- *   y from offsets[E] on are left as they were. offsets and order are read on the device: values
- *   outside their ranges are clamped to them, so a wrong array gives wrong rows, never an access
- *   outside the buffers.
+ *   in sorted order; then rows == S). w: MXFP4 of E*N rows, xm: MXFP4 of `rows` rows;
+ *   E * ceil(S / 16) < 2^31. Rows of y from offsets[E] on are left as they were. offsets and order
+ *   are read on the device: values outside their ranges are clamped to them, so a wrong array
+ *   gives wrong rows, never an access outside the buffers.
  *
  * experts_gather: xs [S][H], xs[slots[t][j]] = x[t]; rows that no slot has are left as they were.
  * experts_combine: y[t] = sum over j of weights[t][j] * ys[slots[t][j]], j upwards, in f32; slots
@@ -295,8 +295,8 @@ int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int
  * experts_combine_grad: dys[slots[t][j]] = weights[t][j] * dy[t] (of ys's type; other rows left as
  *   they were) and dweights f32 [S], dweights[t][j] = <dy[t], ys[slots[t][j]]>, 0 without a row.
  *   In these three, a slots entry outside [0, S) counts as no row; two slots must not name one
- *   row. 1 <= T < 2^24, 1 <= H < 2^28, T*H < 2^35; any element alignment; 16-byte aligned rows are faster. Outputs
- *   must not overlap inputs.
+ *   row. 1 <= T < 2^24, 1 <= H < 2^28, T*H < 2^35; any element alignment; 16-byte aligned
+ *   rows are faster.
  */
 size_t qpg_experts_sort_bytes(int64_t S, int64_t E);
 int experts_sort(const void* ids, int id_bytes, int64_t S, int64_t E, int32_t* offsets, int32_t* order,

@@ -9,6 +9,7 @@ constexpr int64_t kMaxK = (int64_t)1 << 24;
 constexpr int64_t kMaxValues = (int64_t)1 << 35;     // an 8-value thread each: a launch holds < 2^32 threads
 constexpr int64_t kMaxTokens = (int64_t)1 << 24;     // likewise, 256 threads to a token
 constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxSlots = (int64_t)1 << 30;      // a row plus a tile's height is an int
 constexpr int64_t kMaxRow = (int64_t)1 << 28;        // a row's bytes stay below 2^31
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -33,7 +34,7 @@ bool slots_ok(int64_t T, int64_t top_k, int64_t H)
 {
     if (T < 1 || top_k < 1 || H < 1 || T >= kMaxTokens || top_k >= kMaxDim || H >= kMaxRow) return false;
     // the vector lanes of all rows, and a row's segments at one value to a lane
-    return T <= (kMaxDim - 1) / top_k && T <= (kMaxValues - 1) / H;
+    return T <= kMaxSlots / top_k && T <= (kMaxValues - 1) / H;
 }
 
 int quantize(const void* x, int x_type, void* xm, int64_t M, int64_t K, hipStream_t s)
@@ -103,7 +104,7 @@ int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int
 
 size_t qpg_experts_sort_bytes(int64_t S, int64_t E)
 {
-    if (S < 1 || S >= kMaxDim || E < 1 || E > kMaxExperts) return 0;
+    if (S < 1 || S > kMaxSlots || E < 1 || E > kMaxExperts) return 0;
     const int blocks = qpg_experts_sort_blocks(S);
     return blocks > 1 ? (size_t)blocks * (size_t)E * sizeof(int32_t) : 0;
 }
@@ -112,7 +113,7 @@ int experts_sort(const void* ids, int id_bytes, int64_t S, int64_t E, int32_t* o
                  void* ws, qpg_stream_t stream)
 {
     if (!ids || !offsets || !order || !slots || (id_bytes != 4 && id_bytes != 8)) return QPG_EINVAL;
-    if (S < 1 || S >= kMaxDim || E < 1 || E > kMaxExperts) return QPG_EINVAL;
+    if (S < 1 || S > kMaxSlots || E < 1 || E > kMaxExperts) return QPG_EINVAL;
     if (!ws && qpg_experts_sort_bytes(S, E)) return QPG_EINVAL;
     if (!aligned(ids, id_bytes) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(slots, 4) || !aligned(ws, 4))
         return QPG_EALIGN;
@@ -127,7 +128,9 @@ int mmq_mxfp4_experts(const void* w, const void* xm, int64_t rows, const int32_t
                       qpg_stream_t stream)
 {
     if (!w || !xm || !offsets || !y || !type_ok(y_type)) return QPG_EINVAL;
-    if (S < 1 || S >= kMaxDim || E < 1 || E > kMaxExperts || top_k < 1 || top_k >= kMaxDim) return QPG_EINVAL;
+    if (S < 1 || S > kMaxSlots || E < 1 || E > kMaxExperts || top_k < 1 || top_k >= kMaxDim) return QPG_EINVAL;
+    // the row tiles that any offsets can stand for: every expert all S rows
+    if (E * ((S + 15) / 16) >= kMaxDim) return QPG_EINVAL;
     if (!order && rows != S) return QPG_EINVAL;
     if (!mx_shape_ok(rows, K) || N < 1 || N >= kMaxDim || !mx_shape_ok(E * N, K)) return QPG_EINVAL;
     if (((S + 15) / 16 + E) * ((N + 15) / 16) >= kMaxDim) return QPG_EINVAL;

@@ -22,7 +22,8 @@ def test_sizes():
         assert L.qpg_mxfp4_bytes(rows, K) == 0, (rows, K)
     assert L.qpg_experts_sort_bytes(16, 8) == 0
     assert L.qpg_experts_sort_bytes(2 ** 20, 8) > 0
-    for S, E in ((0, 8), (-1, 8), (2 ** 31, 8), (16, 0), (16, 1025), (2 ** 20, 1025)):
+    assert L.qpg_experts_sort_bytes(2 ** 30, 1024) > 0
+    for S, E in ((0, 8), (-1, 8), (2 ** 31, 8), (2 ** 30 + 1, 8), (16, 0), (16, 1025), (2 ** 20, 1025)):
         assert L.qpg_experts_sort_bytes(S, E) == 0
     assert len(R.pack(*R.encode(__import__("numpy").ones((7, 96))))) == B.mxfp4_bytes(7, 96)
 
@@ -43,7 +44,7 @@ CALLS = [
      [(0, 0, EINVAL), (1, 0, EINVAL), (3, 0, EINVAL), (8, 0, EINVAL), (2, 5, EINVAL), (4, 5, EINVAL), (5, 0, EINVAL),
       (6, 0, EINVAL), (7, 31, EINVAL), (0, A + 4, EALIGN), (1, A + 4, EALIGN), (3, A + 1, EALIGN), (8, A + 4, EALIGN)]),
     ("experts_sort", [A, 8, 100, 8, A, A, A, 0, 0],
-     [(0, 0, EINVAL), (1, 2, EINVAL), (2, 0, EINVAL), (2, 2 ** 31, EINVAL), (3, 0, EINVAL), (3, 1025, EINVAL),
+     [(0, 0, EINVAL), (1, 2, EINVAL), (2, 0, EINVAL), (2, 2 ** 31, EINVAL), (2, 2 ** 30 + 1, EINVAL), (3, 0, EINVAL), (3, 1025, EINVAL),
       (4, 0, EINVAL), (5, 0, EINVAL), (6, 0, EINVAL), (2, 2 ** 20, EINVAL), (0, A + 4, EALIGN), (4, A + 2, EALIGN),
       (5, A + 1, EALIGN), (6, A + 2, EALIGN), (7, A + 2, EALIGN)]),
     ("mmq_mxfp4_experts", [A, A, 4, A, A, 2, A, 0, 8, 3, 16, 64, 0],
@@ -51,9 +52,12 @@ CALLS = [
       (5, 0, EINVAL), (8, 0, EINVAL), (9, 0, EINVAL), (9, 1025, EINVAL), (10, 0, EINVAL), (11, 16, EINVAL),
       (10, 2 ** 30, EINVAL), (0, A + 4, EALIGN), (1, A + 4, EALIGN), (3, A + 2, EALIGN), (4, A + 2, EALIGN),
       (6, A + 2, EALIGN)]),
+    # slots past 2^30 (a row and a tile's height past an int), and more tiles than an int counts
+    ("mmq_mxfp4_experts", [A, A, 4, A, A, 2 ** 29, A, 0, 2 ** 30, 1, 16, 64, 0],
+     [(8, 2 ** 30 + 1, EINVAL), (8, 2 ** 31 - 1, EINVAL), (9, 32, EINVAL)]),
     ("experts_gather", [A, 2, A, A, 4, 2, 64, 0],
      [(0, 0, EINVAL), (2, 0, EINVAL), (3, 0, EINVAL), (1, 3, EINVAL), (4, 0, EINVAL), (5, 0, EINVAL), (6, 0, EINVAL),
-      (5, 2 ** 30, EINVAL), (6, 2 ** 28, EINVAL), (4, 2 ** 24, EINVAL), (0, A + 1, EALIGN), (2, A + 2, EALIGN), (3, A + 1, EALIGN)]),
+      (5, 2 ** 30, EINVAL), (5, 2 ** 28 + 1, EINVAL), (6, 2 ** 28, EINVAL), (4, 2 ** 24, EINVAL), (0, A + 1, EALIGN), (2, A + 2, EALIGN), (3, A + 1, EALIGN)]),
     ("experts_combine", [A, 0, A, A, A, 2, 4, 2, 64, 0],
      [(0, 0, EINVAL), (2, 0, EINVAL), (4, 0, EINVAL), (1, 3, EINVAL), (5, 3, EINVAL), (6, 0, EINVAL), (7, 0, EINVAL),
       (8, 0, EINVAL), (0, A + 2, EALIGN), (2, A + 1, EALIGN), (3, A + 2, EALIGN), (4, A + 1, EALIGN)]),

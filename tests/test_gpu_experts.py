@@ -222,6 +222,18 @@ def test_wrong_arrays_stay_inside_the_buffers():
         B.mmq_mxfp4_experts(w, xm, T, offsets, wild, top_k, E, N, K, y=room[1:-1])
         torch.cuda.synchronize()
         assert bool((room[0] == 5.0).all()) and bool((room[-1] == 5.0).all())
+    # ranges of experts that overlap, in the tiled forms: more tiles than rows stand for
+    for T2, N2 in ((700, 600), (1500, 1400), (2500, 2500)):
+        S2 = T2 * 2
+        w2 = torch.from_numpy(R.weights(4 * N2, K, rng)).to(DEV)
+        xm2 = torch.from_numpy(R.weights(T2, K, rng)).to(DEV)
+        order = torch.arange(S2 - 1, -1, -1, dtype=torch.int32, device=DEV)
+        for off in ([0, S2, 0, S2, 0], [5, 2 ** 31 - 1, -9, S2, S2]):
+            room = torch.full((S2 + 2, N2), 5.0, device=DEV)
+            B.mmq_mxfp4_experts(w2, xm2, T2, torch.tensor(off, dtype=torch.int32, device=DEV), order, 2, 4, N2, K,
+                                y=room[1:-1])
+            torch.cuda.synchronize()
+            assert bool((room[0] == 5.0).all()) and bool((room[-1] == 5.0).all())
     # slots: out of range counts as no row
     slots = torch.full((T, top_k), -1, dtype=torch.int32, device=DEV)
     slots[0, 0], slots[1, 1], slots[2, 0] = S, 2 ** 31 - 1, -2 ** 31
