@@ -236,13 +236,13 @@ int mmq_q6K_exp_q8_sk(const void* we, const void* xq, float* y, int64_t M, int64
  * Element types of float arguments (x_type, y_type, ...): QPG_F32, QPG_F16, QPG_BF16; any other
  * value is QPG_EINVAL. Arithmetic and sums are f32; a result is rounded once, to nearest
  * even, when it is stored. Shapes of this section: 1 <= M, N < 2^31; 32 <= K <= 2^24,
- * K % 32 == 0 (K / 32 need not be even or a multiple of anything), rows*K < 2^35 of every
- * operand; the number of tiles of 16 x 16 outputs must be < 2^31. A product that would need
+ * K % 32 == 0 (K / 32 need not be even or a multiple of anything), rows*K <= 2^35 - 2^11 of
+ * every operand; the number of tiles of 16 x 16 outputs must be < 2^31. A product that would need
  * more threads than a launch holds (N > 2^24 with many tokens) is QPG_EINVAL.
  */
 enum { QPG_F32 = 0, QPG_F16 = 1, QPG_BF16 = 2 };
 
-/* rows*K/2 + rows*K/32; 0 for an unsupported shape (rows < 1, rows >= 2^31, K as above, rows*K >= 2^35). */
+/* rows*K/2 + rows*K/32; 0 for an unsupported shape (rows < 1, rows >= 2^31, K as above, rows*K > 2^35 - 2^11). */
 size_t qpg_mxfp4_bytes(int64_t rows, int64_t K);
 
 /*
@@ -295,8 +295,8 @@ int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int
  * experts_combine_grad: dys[slots[t][j]] = weights[t][j] * dy[t] (of ys's type; other rows left as
  *   they were) and dweights f32 [S], dweights[t][j] = <dy[t], ys[slots[t][j]]>, 0 without a row.
  *   In these three, a slots entry outside [0, S) counts as no row; two slots must not name one
- *   row. 1 <= T < 2^24, 1 <= H < 2^28, T*H < 2^35; any element alignment; 16-byte aligned
- *   rows are faster.
+ *   row. 1 <= T < 2^24, 1 <= H < 2^28, T*H <= 2^35 - 2^11; any element alignment;
+ *   16-byte aligned rows are faster.
  */
 size_t qpg_experts_sort_bytes(int64_t S, int64_t E);
 int experts_sort(const void* ids, int id_bytes, int64_t S, int64_t E, int32_t* offsets, int32_t* order,

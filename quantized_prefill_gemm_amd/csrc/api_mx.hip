@@ -6,7 +6,8 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxK = (int64_t)1 << 24;
-constexpr int64_t kMaxValues = (int64_t)1 << 35;     // an 8-value thread each: a launch holds < 2^32 threads
+// A thread takes 8 values, a launch holds < 2^32 threads in whole workgroups of 256.
+constexpr int64_t kMaxValues = ((int64_t)1 << 35) - (1 << 11);
 constexpr int64_t kMaxTokens = (int64_t)1 << 24;     // likewise, 256 threads to a token
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxSlots = (int64_t)1 << 30;      // a row plus a tile's height is an int
@@ -22,7 +23,7 @@ int status_of(hipError_t e)
 
 bool mx_shape_ok(int64_t rows, int64_t K)
 {
-    return rows >= 1 && rows < kMaxDim && K >= 32 && K % 32 == 0 && K <= kMaxK && rows <= (kMaxValues - 1) / K;
+    return rows >= 1 && rows < kMaxDim && K >= 32 && K % 32 == 0 && K <= kMaxK && rows <= kMaxValues / K;
 }
 
 bool product_shape_ok(int64_t M, int64_t N, int64_t K)
@@ -34,7 +35,7 @@ bool slots_ok(int64_t T, int64_t top_k, int64_t H)
 {
     if (T < 1 || top_k < 1 || H < 1 || T >= kMaxTokens || top_k >= kMaxDim || H >= kMaxRow) return false;
     // the vector lanes of all rows, and a row's segments at one value to a lane
-    return T <= kMaxSlots / top_k && T <= (kMaxValues - 1) / H;
+    return T <= kMaxSlots / top_k && T <= kMaxValues / H;
 }
 
 int quantize(const void* x, int x_type, void* xm, int64_t M, int64_t K, hipStream_t s)

@@ -17,8 +17,9 @@ def test_sizes():
     L = B.lib()
     assert L.qpg_mxfp4_bytes(1, 32) == 17 and L.qpg_mxfp4_bytes(7, 96) == 7 * 51
     assert L.qpg_mxfp4_bytes(512, 4096) == 512 * 4096 * 17 // 32
-    assert L.qpg_mxfp4_bytes(2 ** 30 - 1, 32) == (2 ** 30 - 1) * 17
-    for rows, K in ((0, 32), (-1, 32), (1, 0), (1, 16), (1, 48), (2 ** 31, 32), (1, 2 ** 24 + 32), (2 ** 15, 2 ** 20), (2 ** 30, 32)):
+    assert L.qpg_mxfp4_bytes(2 ** 30 - 64, 32) == (2 ** 30 - 64) * 17
+    for rows, K in ((0, 32), (-1, 32), (1, 0), (1, 16), (1, 48), (2 ** 31, 32), (1, 2 ** 24 + 32), (2 ** 15, 2 ** 20), (2 ** 30 - 63, 32),
+                    (2 ** 30, 32)):
         assert L.qpg_mxfp4_bytes(rows, K) == 0, (rows, K)
     assert L.qpg_experts_sort_bytes(16, 8) == 0
     assert L.qpg_experts_sort_bytes(2 ** 20, 8) > 0

@@ -306,6 +306,90 @@ def test_operators_together_and_in_a_graph(T, top_k, E, N, K, how):
         assert torch.equal(out, layer(i, a, wd, b, E, N, K, torch.float32)), rep
 
 
+@pytest.mark.parametrize("T,top_k,E,H,kind", [(3, 2, 4, 40, "float32"), (2100, 3, 40, 520, "bfloat16"),
+                                              (700, 9, 8, 1001, "float16")])
+def test_training_operators_in_a_graph_and_on_a_stream(T, top_k, E, H, kind):
+    """Sort (with its workspace), gather, weighted sum and all gradients: on two streams at once, and
+    captured and replayed with other routings and values, against the calls one by one."""
+    rng = np.random.default_rng([T, 6])
+
+    def inputs():
+        return (torch.from_numpy(routing(T, top_k, E, rng, "drop")).to(DEV),
+                torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).to(KINDS[kind]).to(DEV),
+                torch.from_numpy(rng.random((T, top_k)).astype(np.float32)).to(DEV))
+
+    def chain(ids, x, wts, ws, stream=None):
+        with torch.cuda.stream(stream):                          # rows that no choice has: zeros
+            xs, dys = torch.zeros((2, T * top_k, H), dtype=x.dtype, device=DEV)
+        offsets, order, slots = B.experts_sort(ids, E, ws=ws, stream=stream)
+        B.experts_gather(x, slots, xs, stream=stream)
+        y = B.experts_combine(xs, slots, wts, stream=stream)
+        _, dw = B.experts_combine_grad(y, xs, slots, wts, dys=dys, stream=stream)
+        dx = B.experts_gather_grad(dys, slots, stream=stream)
+        return [offsets, order, slots, xs, y, dys, dw, dx]
+
+    def workspace():
+        return torch.empty(B.experts_sort_bytes(T * top_k, E) + 4, dtype=torch.uint8, device=DEV)
+
+    pair = [inputs(), inputs()]
+    want = [chain(*a, workspace()) for a in pair]
+    spaces = [workspace(), workspace()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for rep in range(3):
+        got = [chain(*a, ws, stream=streams[(i + rep) % 2]) for i, (a, ws) in enumerate(zip(pair, spaces))]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(u, v) for u, v in zip(a, b)), rep
+
+    held, ws = [t.clone() for t in pair[0]], workspace()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = chain(*held, ws)
+    for rep in range(4):
+        new = inputs()
+        for t, n in zip(held, new):
+            t.copy_(n)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, chain(*new, workspace()))), rep
+
+
+@pytest.mark.parametrize("T,top_k,E,H,kind", [(2 ** 24 - 1, 1, 1024, 1, "float32"), (1, 2, 3, 2 ** 26 + 1, "float16"),
+                                              (2, 300, 5, 70_001, "bfloat16")])
+def test_many_tokens_long_rows_and_many_choices(T, top_k, E, H, kind):
+    """Small whole numbers: every product and sum is exact (f32 holds those below 2^24, the 16-bit
+    types those below 2^8)."""
+    say(f"[rows {T} x {top_k} of {E}, H {H}]")
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    def whole(shape, below, dtype):
+        return torch.randint(-below, below + 1, shape, generator=gen, device=DEV).to(dtype)
+    ids = torch.randint(-1, E, (T, top_k), generator=gen, device=DEV)
+    offsets, order, slots = B.experts_sort(ids, E)
+    n, S = int(offsets[-1]), T * top_k
+    assert n == int((ids >= 0).sum())
+    at = order[:n].long()
+    sorted_ids = ids.view(-1)[at]
+    assert bool((slots.view(-1)[at] == torch.arange(n, device=DEV)).all()) and bool((sorted_ids.diff() >= 0).all())
+    assert bool((at.diff()[sorted_ids.diff() == 0] > 0).all()) and bool((order[n:] == -1).all())
+    x = whole((T, H), 100, KINDS[kind])
+    xs = torch.zeros((S, H), dtype=x.dtype, device=DEV)
+    B.experts_gather(x, slots, xs)
+    assert torch.equal(xs[:n], x[at // top_k]) and not bool(xs[n:].any())
+    ys, wts, dy = whole((S, H), 1, x.dtype), whole((T, top_k), 1, torch.float32), whole((T, H), 1, x.dtype)
+    # torch adds in another order: of whole numbers that is the same
+    scaled = ys[:n].float() * wts.view(-1)[at][:, None]
+    y = torch.zeros((T, H), device=DEV).index_add_(0, at // top_k, scaled)
+    assert torch.equal(B.experts_combine(ys, slots, wts, dtype=torch.float32), y)
+    dys, dw = B.experts_combine_grad(dy, ys, slots, wts, dys=torch.zeros_like(ys))
+    assert torch.equal(dys[:n].float(), wts.view(-1)[at][:, None] * dy[at // top_k].float())
+    dots = torch.zeros(S, device=DEV)
+    dots[at] = (dy[at // top_k].double() * ys[:n].double()).sum(dim=1).float()
+    assert torch.equal(dw.view(-1), dots)
+
+
 def test_refusals():
     ids = torch.zeros((4, 2), dtype=torch.int64, device=DEV)
     offsets, order, slots = B.experts_sort(ids, 3)

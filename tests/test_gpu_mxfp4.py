@@ -96,7 +96,8 @@ SHAPES = [(1, 1, 32), (1, 4096, 4096), (2, 7, 96), (15, 100, 544), (16, 256, 512
           (129, 255, 1280), (200, 640, 2080), (257, 513, 1312), (512, 256, 256), (300, 1030, 4096), (700, 900, 2912),
           (200, 1500, 544), (190, 1600, 640), (200, 1501, 800), (513, 2050, 1024), (600, 2100, 288), (300, 40000, 320),
           (200, 1500, 32), (300, 1300, 96), (600, 2100, 64), (600, 2100, 256), (10, 20000, 288), (30, 40000, 480),
-          (3000, 3100, 768), (4200, 4200, 544), (2600, 4097, 640), (2600, 4100, 128)]
+          (3000, 3100, 768), (4200, 4200, 544), (2600, 4097, 640), (2600, 4100, 128), (1100, 2101, 544), (2000, 2900, 1056),
+          (1900, 2100, 32), (1100, 9000, 288)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -128,7 +129,7 @@ def test_product_from_narrow_activations(M, N, K, kind):
 
 
 @pytest.mark.parametrize("M,N,K", [(3, 40, 1120), (40, 72, 1120), (200, 300, 1120), (250, 1400, 1120), (250, 1400, 896),
-                                   (600, 2100, 1120), (3000, 3100, 640)])
+                                   (600, 2100, 1120), (3000, 3100, 640), (1100, 2100, 1120)])
 def test_scales_of_any_size_and_nan(M, N, K):
     """Scale bytes over the whole range a product stays finite in, and NaN scales: a NaN block
     of x makes its row of y NaN, one of w its column, and nothing else."""
@@ -150,7 +151,7 @@ def test_scales_of_any_size_and_nan(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(5, 37, 160), (70, 131, 1056), (300, 257, 544), (300, 1301, 544), (601, 2100, 544),
-                                   (3001, 3100, 544)])
+                                   (3001, 3100, 544), (1101, 2100, 544)])
 def test_nothing_outside_the_outputs_is_written(M, N, K):
     w, x = product_case(M, N, K, 3)
     wd, xd = torch.from_numpy(w).to(DEV), x.to(DEV)
@@ -169,7 +170,8 @@ def test_nothing_outside_the_outputs_is_written(M, N, K):
     assert bool((room[:32] == 5.0).all()) and bool((room[32 + M * K:] == 5.0).all())
 
 
-@pytest.mark.parametrize("M,N,K", [(21, 50, 1056), (250, 1400, 1056), (250, 1400, 1152), (600, 2100, 1056)])
+@pytest.mark.parametrize("M,N,K", [(21, 50, 1056), (250, 1400, 1056), (250, 1400, 1152), (600, 2100, 1056), (1100, 2100, 1056),
+                                   (2600, 4100, 1056)])
 def test_operand_at_the_end_of_its_buffer(M, N, K):
     """The last rows' partial units: the result does not depend on what follows the operands
     (scale bytes of NaN right behind both planes)."""
@@ -182,6 +184,41 @@ def test_operand_at_the_end_of_its_buffer(M, N, K):
     roomx = torch.full((xm.numel() + 256,), 255, dtype=torch.uint8, device=DEV)
     roomx[: xm.numel()] = xm
     assert torch.equal(B.mmq_mxfp4_mx(room, roomx, M, N, K), y)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 1056), (4, 300, 480), (16, 33, 992), (16, 1000, 1024), (14, 2000, 1120)])
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_few_tokens_with_nan_and_infinity(M, N, K, kind):
+    """From floats, a block with a NaN or an infinity makes its token's outputs NaN and no other's."""
+    w, x = product_case(M, N, K, 8, kind)
+    x[M - 1, K - 1] = float("inf")
+    if M > 3:
+        x[2, 33] = float("nan")
+        x[0, :32] = 0
+    wd, xd = torch.from_numpy(w).to(DEV), x.to(DEV)
+    ws = torch.empty(B.mxfp4_bytes(M, K), dtype=torch.uint8, device=DEV)
+    y = B.mmq_mxfp4(wd, xd, N, xm_ws=ws)
+    assert torch.equal(ws, B.quantize_mxfp4(xd))
+    lost = [m for m in range(M) if m == M - 1 or (M > 3 and m == 2)]
+    kept = [m for m in range(M) if m not in lost]
+    assert bool(torch.isnan(y[lost]).all()) and not bool(torch.isnan(y[kept]).any())
+    assert torch.equal(y[kept], B.mmq_mxfp4_mx(wd, ws, M, N, K)[kept])
+
+
+# Ones times powers of two: every sum is a multiple of the power below 2^24 times it, exact in f32.
+@pytest.mark.parametrize("M,N,K", [(1, 40, 2 ** 24), (140, 2040, 2 ** 24), (1, 2 ** 24 + 40, 64), (20, 2 ** 24 + 40, 32),
+                                   (2 ** 20 + 3, 520, 32)])
+def test_longest_rows_and_widest_outputs(M, N, K):
+    say(f"[product {M} x {N} x {K}]")
+    def ones(rows):
+        b = torch.full((B.mxfp4_bytes(rows, K),), 0x22, dtype=torch.uint8, device=DEV)
+        power = torch.arange(rows, device=DEV) % 5
+        b[rows * K // 2:].view(rows, K // 32).copy_((125 + power).to(torch.uint8)[:, None].expand(rows, K // 32))
+        return b, torch.ldexp(torch.ones(rows, device=DEV), power.int() - 2)
+    w, wp = ones(N)
+    x, xp = ones(M)
+    y = B.mmq_mxfp4_mx(w, x, M, N, K)
+    assert bool((y == xp[:, None] * (wp * K)[None]).all())
 
 
 def test_rows_past_32_bit_offsets():
