@@ -168,7 +168,8 @@ PRODUCTS = [(1, 1, 1, 1, 32, "uniform"), (4, 4, 32, 300, 1056, "uniform"), (3, 2
             (40, 2, 3, 130, 544, "skew"), (64, 1, 4, 64, 512, "one"), (200, 2, 4, 260, 992, "drop"), (9, 3, 5, 50, 64, "none"),
             (700, 2, 5, 200, 1312, "skew"), (600, 1, 2, 513, 768, "drop"), (100, 4, 200, 48, 160, "uniform"),
             (1500, 1, 4, 1400, 544, "skew"), (3000, 2, 3, 2100, 768, "drop"), (2500, 2, 3, 2500, 640, "skew"),
-            (300, 2, 40, 300, 800, "uniform"), (4, 4, 32, 1100, 1056, "drop"), (200, 2, 12, 3000, 288, "uniform")]
+            (300, 2, 40, 300, 800, "uniform"), (4, 4, 32, 1100, 1056, "drop"), (200, 2, 12, 3000, 288, "uniform"),
+            (3000, 2, 3, 4200, 544, "drop"), (2300, 2, 7, 2304, 160, "uniform")]
 
 
 @pytest.mark.parametrize("T,top_k,E,N,K,how", PRODUCTS)

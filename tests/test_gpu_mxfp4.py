@@ -97,7 +97,7 @@ SHAPES = [(1, 1, 32), (1, 4096, 4096), (2, 7, 96), (15, 100, 544), (16, 256, 512
           (200, 1500, 544), (190, 1600, 640), (200, 1501, 800), (513, 2050, 1024), (600, 2100, 288), (300, 40000, 320),
           (200, 1500, 32), (300, 1300, 96), (600, 2100, 64), (600, 2100, 256), (10, 20000, 288), (30, 40000, 480),
           (3000, 3100, 768), (4200, 4200, 544), (2600, 4097, 640), (2600, 4100, 128), (1100, 2101, 544), (2000, 2900, 1056),
-          (1900, 2100, 32), (1100, 9000, 288)]
+          (1900, 2100, 32), (1100, 9000, 288), (4360, 4352, 288)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -151,7 +151,7 @@ def test_scales_of_any_size_and_nan(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(5, 37, 160), (70, 131, 1056), (300, 257, 544), (300, 1301, 544), (601, 2100, 544),
-                                   (3001, 3100, 544), (1101, 2100, 544)])
+                                   (3001, 3100, 544), (1101, 2100, 544), (4201, 4203, 160)])
 def test_nothing_outside_the_outputs_is_written(M, N, K):
     w, x = product_case(M, N, K, 3)
     wd, xd = torch.from_numpy(w).to(DEV), x.to(DEV)
