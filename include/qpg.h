@@ -25,9 +25,10 @@
  *     and the device are checked before anything is enqueued, so on QPG_EINVAL,
  *     QPG_EALIGN and QPG_EDEVICE nothing has been. QPG_EHIP reports a failed kernel
  *     launch; in the entry points that enqueue two kernels (mmq_q4K / mmq_q6K: quantise,
- *     then the MMQ; the _sk entry points with a split: the MMQ, then the reduce) the first
- *     may already be enqueued when the second fails. QPG_ESCRATCH (mmq_q4K_noalloc only)
- *     is reported before anything is enqueued. There is no fallback path.
+ *     then the MMQ; the _sk entry points with a split: the MMQ, then the reduce; mmq_mxfp4 and
+ *     experts_sort likewise) the first may already be enqueued when the second fails.
+ *     QPG_ESCRATCH (mmq_q4K_noalloc only) is reported before anything is enqueued. There is no
+ *     fallback path.
  *   - The library runs on gfx950 only (QPG_EDEVICE otherwise).
  *
  * Data layouts
@@ -237,8 +238,7 @@ int mmq_q6K_exp_q8_sk(const void* we, const void* xq, float* y, int64_t M, int64
  * value is QPG_EINVAL. Arithmetic and sums are f32; a result is rounded once, to nearest
  * even, when it is stored. Shapes of this section: 1 <= M, N < 2^31; 32 <= K <= 2^24,
  * K % 32 == 0 (K / 32 need not be even or a multiple of anything), rows*K <= 2^35 - 2^11 of
- * every operand; the number of tiles of 16 x 16 outputs must be < 2^31. A product that would need
- * more threads than a launch holds (N > 2^24 with many tokens) is QPG_EINVAL.
+ * every operand; the number of tiles of 16 x 16 outputs must be < 2^31.
  */
 enum { QPG_F32 = 0, QPG_F16 = 1, QPG_BF16 = 2 };
 

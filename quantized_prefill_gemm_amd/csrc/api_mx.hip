@@ -15,11 +15,7 @@ constexpr int64_t kMaxRow = (int64_t)1 << 28;        // a row's bytes stay below
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 bool type_ok(int t) { return t == QPG_F32 || t == QPG_F16 || t == QPG_BF16; }
-// hipErrorInvalidConfiguration: the launcher's own refusal of more threads than a launch holds.
-int status_of(hipError_t e)
-{
-    return e == hipSuccess ? QPG_OK : e == hipErrorInvalidConfiguration ? QPG_EINVAL : QPG_EHIP;
-}
+int status_of(hipError_t e) { return e == hipSuccess ? QPG_OK : QPG_EHIP; }
 
 bool mx_shape_ok(int64_t rows, int64_t K)
 {

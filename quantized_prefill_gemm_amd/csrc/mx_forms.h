@@ -28,6 +28,20 @@ constexpr FormShape form_shape(Form form)
     }
 }
 
+// Grid of a streaming form: a launch holds < 2^32 threads along x, so tiles past STREAM_GRID_X
+// go on in further rows of the grid (fewer than 2^31 tiles: at most 512 rows).
+constexpr int64_t STREAM_GRID_X = (int64_t)1 << 22;
+
+struct StreamGrid {
+    unsigned x, y;
+};
+
+inline StreamGrid stream_grid(int64_t tiles)
+{
+    const int64_t x = tiles < STREAM_GRID_X ? tiles : STREAM_GRID_X;
+    return {(unsigned)x, (unsigned)((tiles + x - 1) / x)};
+}
+
 // The form for `groups` matrices of N rows and `rows` tokens each (dense: one group; experts: the
 // mean). Measured with weights from HBM, f32 out, M x N x K or tokens x
 // top_k x experts x N x K, us:
