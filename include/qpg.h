@@ -232,7 +232,8 @@ int mmq_q6K_exp_q8_sk(const void* we, const void* xq, float* y, int64_t M, int64
  *                             one of 0, 0.5, 1, 1.5, 2, 3, 4, 6.
  *       then rows*K/32 bytes: scales [rows][K/32], e = 2^(e - 127), 255 = NaN.
  *     16-byte aligned. Activations and weights have the same layout; the matrices of E experts
- *     are one buffer of E*N rows.
+ *     are one buffer of E*N rows. The scales' place follows from `rows`: a buffer of more rows is
+ *     no buffer of its first ones.
  *
  * Element types of float arguments (x_type, y_type, ...): QPG_F32, QPG_F16, QPG_BF16; any other
  * value is QPG_EINVAL. Arithmetic and sums are f32; a result is rounded once, to nearest

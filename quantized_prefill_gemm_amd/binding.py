@@ -422,11 +422,24 @@ def _is(t: torch.Tensor, dtype, shape, name: str, ref: torch.Tensor):
 
 
 def _mx(t: torch.Tensor, rows: int, K: int, name: str, ref: torch.Tensor):
-    """An MXFP4 operand of rows x K values (uint8, at least its size)."""
+    """An MXFP4 operand of rows x K values: uint8, at least its size. Activations may lie in a
+    workspace for more tokens; the scales follow the codes of `rows` rows there too."""
     need = _mx_bytes(rows, K, name)
     if t.dtype is not torch.uint8 or t.get_device() != ref.get_device() or t.get_device() < 0 \
             or not t.is_contiguous() or t.numel() < need:
         _out(t, torch.uint8, name, need, ref)
+
+
+def _mx_weights(w: torch.Tensor, rows: int, K: int, ref: torch.Tensor):
+    """MXFP4 weights of rows x K values. The scales start where the codes of all rows end, so the
+    buffer of a matrix of more rows is no buffer of its first ones: a size of a whole number of
+    other rows is refused. (Bytes behind the matrix that make up no rows are let pass.)"""
+    if w.numel() == mxfp4_bytes(rows, K) and w.dtype is torch.uint8 and w.get_device() == ref.get_device() >= 0 \
+            and w.is_contiguous():
+        return
+    _mx(w, rows, K, "w", ref)
+    if w.numel() != mxfp4_bytes(rows, K) and w.numel() * 32 % (17 * K) == 0:
+        raise QPGError(QPG_EINVAL, f"w is the size of {w.numel() * 32 // (17 * K)} x {K} MXFP4 values, not of {rows} x {K}")
 
 
 @functools.lru_cache(maxsize=4096)
@@ -486,7 +499,7 @@ def mmq_mxfp4(w: torch.Tensor, x: torch.Tensor, N: int, y=None, xm_ws=None, dtyp
     x_code = _float(x, "x")
     M, K = x.shape
     nbytes = _mx_bytes(M, K, "x")
-    _mx(w, N, K, "w", x)
+    _mx_weights(w, N, K, x)
     dtype, y_code = _given(y, dtype, (M, N), "y", x)
     if xm_ws is not None:
         _mx(xm_ws, M, K, "xm_ws", x)
@@ -504,7 +517,7 @@ def mmq_mxfp4_mx(w: torch.Tensor, xm: torch.Tensor, M: int, N: int, K: int, y=No
                  stream=None) -> torch.Tensor:
     """y [M, N] = xm [M, K] x w [N, K]^T, both MXFP4 buffers."""
     _mx(xm, M, K, "xm", xm)
-    _mx(w, N, K, "w", xm)
+    _mx_weights(w, N, K, xm)
     dtype, code = _given(y, dtype, (M, N), "y", xm)
 
     def call(s):
@@ -562,7 +575,7 @@ def mmq_mxfp4_experts(w: torch.Tensor, xm: torch.Tensor, rows: int, offsets: tor
     order None the rows in sorted order themselves (S = rows). Rows of y behind the last
     (offsets[E]) are not written."""
     _mx(xm, rows, K, "xm", xm)
-    _mx(w, E * N, K, "w", xm)
+    _mx_weights(w, E * N, K, xm)
     _is(offsets, torch.int32, (E + 1,), "offsets", xm)
     S = rows if order is None else order.numel()
     if order is not None:
