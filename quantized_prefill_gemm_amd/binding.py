@@ -571,14 +571,15 @@ def experts_sort(ids: torch.Tensor, E: int, offsets=None, order=None, slots=None
 def mmq_mxfp4_experts(w: torch.Tensor, xm: torch.Tensor, rows: int, offsets: torch.Tensor, order, top_k: int, E: int,
                       N: int, K: int, y=None, dtype=torch.float32, stream=None) -> torch.Tensor:
     """y[p] = activation row x w[expert of p]^T for every sorted row p. w: MXFP4 of E * N rows, xm:
-    MXFP4 of `rows` rows -- the tokens, read through order [S] (row order[p] // top_k), or with
-    order None the rows in sorted order themselves (S = rows). Rows of y behind the last
-    (offsets[E]) are not written."""
+    MXFP4 of `rows` rows -- the tokens, read through order [S], S = rows * top_k (row order[p] //
+    top_k; tokens that only pad a batch have choices outside [0, E)), or with order None the rows
+    in sorted order themselves (S = rows). Rows of y behind the last (offsets[E]) are not written."""
     _mx(xm, rows, K, "xm", xm)
     _mx_weights(w, E * N, K, xm)
     _is(offsets, torch.int32, (E + 1,), "offsets", xm)
-    S = rows if order is None else order.numel()
+    S = rows
     if order is not None:
+        S *= top_k
         _is(order, torch.int32, (S,), "order", xm)
     dtype, code = _given(y, dtype, (S, N), "y", xm)
 

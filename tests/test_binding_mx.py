@@ -77,3 +77,17 @@ def test_weights_of_another_number_of_rows(run, N, K):
     assert run(lambda: B.mmq_mxfp4(u8(size(N)), x, N, xm_ws=u8(size(64)))) == "called"
     assert run(lambda: B.mmq_mxfp4_experts(u8(size(3 * N)), xm, 4, i32(4), i32(8), 2, 3, N, K)) == "called"
     assert run(lambda: B.mmq_mxfp4_experts(u8(size(4 * N)), xm, 4, i32(4), i32(8), 2, 3, N, K)) == B.QPG_EINVAL
+
+
+def test_order_of_another_number_of_choices(run):
+    """order has rows * top_k entries: with another top_k, or xm of another number of tokens, rows
+    would be taken from the wrong tokens."""
+    E, N, K, T = 3, 16, 64, 6
+    w, xm = u8(B.mxfp4_bytes(E * N, K)), u8(B.mxfp4_bytes(T, K))
+
+    def call(order, top_k, rows=T):
+        return run(lambda: B.mmq_mxfp4_experts(w, xm, rows, i32(E + 1), order, top_k, E, N, K))
+    assert call(i32(12), 2) == "called" and call(None, 1) == "called" and call(i32(6), 1) == "called"
+    for order, top_k in ((i32(12), 1), (i32(12), 3), (i32(12), 4), (i32(12), 0), (i32(12), -2), (i32(6, 2), 2), (i32(11), 2)):
+        assert call(order, top_k) == B.QPG_EINVAL, (order.shape, top_k)
+    assert call(i32(12), 2, rows=5) == B.QPG_EINVAL and call(i32(12), 3, rows=4) == "called"
