@@ -380,7 +380,14 @@ def mmq_q6K_exp_q8_sk(we, xq, M, N, K, y=None, ws=None, stream=None):
 # A small call is bound by the host (a launch takes 3.7 us, torch.cuda.current_stream() 2.9, an
 # allocation 1.4), so the checks below are one comparison each where nothing is wrong.
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}      # QPG_F32, QPG_F16, QPG_BF16
-_raw_stream = torch._C._cuda_getCurrentRawStream                      # current_stream().cuda_stream, 0.1 us
+
+
+def _current_raw_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# 0.1 us where torch has it (a torch built without a GPU backend does not, and still loads this module)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw_stream)
 
 
 def _run(t: torch.Tensor, stream, call):

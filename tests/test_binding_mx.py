@@ -1,6 +1,8 @@
 """What the binding of the MXFP4 and expert operators refuses by itself, before the library is
 called (on the CPU, with stand-ins that have a device tensor's type, shape and place)."""
 import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -91,3 +93,16 @@ def test_order_of_another_number_of_choices(run):
     for order, top_k in ((i32(12), 1), (i32(12), 3), (i32(12), 4), (i32(12), 0), (i32(12), -2), (i32(6, 2), 2), (i32(11), 2)):
         assert call(order, top_k) == B.QPG_EINVAL, (order.shape, top_k)
     assert call(i32(12), 2, rows=5) == B.QPG_EINVAL and call(i32(12), 3, rows=4) == "called"
+
+
+def test_imports_on_a_torch_without_a_gpu_backend():
+    """The module, and with it the host entry points of every operator, loads where torch has no
+    _cuda_getCurrentRawStream."""
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'): del torch._C._cuda_getCurrentRawStream\n"
+            "import quantized_prefill_gemm_amd as qpg\n"
+            "print(qpg.q8_1_bytes(1, 256), qpg.mxfp4_bytes(1, 64))\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(B.__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr
+    assert out.stdout.split() == [str(B.q8_1_bytes(1, 256)), "34"]
