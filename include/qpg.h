@@ -25,8 +25,8 @@
  *     and the device are checked before anything is enqueued, so on QPG_EINVAL,
  *     QPG_EALIGN and QPG_EDEVICE nothing has been. QPG_EHIP reports a failed kernel
  *     launch; in the entry points that enqueue two kernels (mmq_q4K / mmq_q6K: quantise,
- *     then the MMQ; the _sk entry points with a split: the MMQ, then the reduce; mmq_mxfp4 and
- *     experts_sort likewise) the first may already be enqueued when the second fails.
+ *     then the MMQ; the _sk entry points with a split: the MMQ, then the reduce; mmq_mxfp4, experts_sort
+ *     and the _zero entry points likewise) the first may already be enqueued when the second fails.
  *     QPG_ESCRATCH (mmq_q4K_noalloc only) is reported before anything is enqueued. There is no
  *     fallback path.
  *   - The library runs on gfx950 only (QPG_EDEVICE otherwise).
@@ -295,7 +295,9 @@ int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int
  *   experts_gather, dx[t] = sum over j of dxs[slots[t][j]].
  * experts_combine_grad: dys[slots[t][j]] = weights[t][j] * dy[t] (of ys's type; other rows left as
  *   they were) and dweights f32 [S], dweights[t][j] = <dy[t], ys[slots[t][j]]>, 0 without a row.
- *   In these three, a slots entry outside [0, S) counts as no row; two slots must not name one
+ * experts_gather_zero, experts_combine_grad_zero: the same, and the rows of xs or dys that no slot has
+ *   become zeros (by two kernels where there are many slots of short rows).
+ *   In all of these, a slots entry outside [0, S) counts as no row; two slots must not name one
  *   row. 1 <= T < 2^24, 1 <= H < 2^28, T*H <= 2^35 - 2^11; any element alignment;
  *   16-byte aligned rows are faster.
  */
@@ -307,11 +309,16 @@ int mmq_mxfp4_experts(const void* w, const void* xm, int64_t rows, const int32_t
                       qpg_stream_t stream);
 int experts_gather(const void* x, int type, const int32_t* slots, void* xs, int64_t T, int64_t top_k, int64_t H,
                    qpg_stream_t stream);
+int experts_gather_zero(const void* x, int type, const int32_t* slots, void* xs, int64_t T, int64_t top_k, int64_t H,
+                        qpg_stream_t stream);
 int experts_combine(const void* ys, int ys_type, const int32_t* slots, const float* weights, void* y, int y_type,
                     int64_t T, int64_t top_k, int64_t H, qpg_stream_t stream);
 int experts_combine_grad(const void* dy, int dy_type, const void* ys, int ys_type, const int32_t* slots,
                          const float* weights, void* dys, float* dweights, int64_t T, int64_t top_k, int64_t H,
                          qpg_stream_t stream);
+int experts_combine_grad_zero(const void* dy, int dy_type, const void* ys, int ys_type, const int32_t* slots,
+                              const float* weights, void* dys, float* dweights, int64_t T, int64_t top_k, int64_t H,
+                              qpg_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -75,8 +75,10 @@ def lib() -> ctypes.CDLL:
                 (L.mmq_mxfp4_experts, INT, [P, P, I64, P, P, I64, P, INT, I64, I64, I64, I64, P]),
                 (L.experts_sort, INT, [P, INT, I64, I64, P, P, P, P, P]),
                 (L.experts_gather, INT, [P, INT, P, P, I64, I64, I64, P]),
+                (L.experts_gather_zero, INT, [P, INT, P, P, I64, I64, I64, P]),
                 (L.experts_combine, INT, [P, INT, P, P, P, INT, I64, I64, I64, P]),
-                (L.experts_combine_grad, INT, [P, INT, P, INT, P, P, P, P, I64, I64, I64, P])):
+                (L.experts_combine_grad, INT, [P, INT, P, INT, P, P, P, P, I64, I64, I64, P]),
+                (L.experts_combine_grad_zero, INT, [P, INT, P, INT, P, P, P, P, I64, I64, I64, P])):
             f.restype, f.argtypes = res, args
         _lib = L
     return _lib
@@ -88,7 +90,8 @@ EXPORTS = ("qpg_strerror", "qpg_q8_1_bytes", "quantize_q8_1", "mmq_q4K", "mmq_q6
            "mmq_q6K_exp_csums", "qpg_mmq_sk_bytes", "mmq_q4K_q8_sk", "mmq_q6K_q8_sk", "mmq_q6K_prep_q8_sk",
            "mmq_q6K_exp_q8_sk", "mmq_q4K_noalloc", "qpg_mxfp4_bytes", "quantize_mxfp4", "dequantize_mxfp4",
            "mmq_mxfp4_mx", "mmq_mxfp4", "qpg_experts_sort_bytes", "experts_sort", "mmq_mxfp4_experts",
-           "experts_gather", "experts_combine", "experts_combine_grad")
+           "experts_gather", "experts_gather_zero", "experts_combine", "experts_combine_grad",
+           "experts_combine_grad_zero")
 
 
 def _check(rc: int, what: str):
@@ -609,7 +612,8 @@ def _slots(slots: torch.Tensor, ref: torch.Tensor):
 
 
 def experts_gather(x: torch.Tensor, slots: torch.Tensor, xs=None, stream=None) -> torch.Tensor:
-    """xs [T * top_k, H]: row slots[t, j] is x[t]. Rows that no choice has are not written."""
+    """xs [T * top_k, H]: row slots[t, j] is x[t]. Rows that no choice has are not written in an xs
+    that is given, zeros in one allocated here."""
     code = _float(x, "x")
     T, top_k = _slots(slots, x)
     H = x.shape[1]
@@ -619,9 +623,10 @@ def experts_gather(x: torch.Tensor, slots: torch.Tensor, xs=None, stream=None) -
         _is(xs, x.dtype, (T * top_k, H), "xs", x)
 
     def call(s):
-        out = torch.empty((T * top_k, H), dtype=x.dtype, device=x.device) if xs is None else xs
-        _check(lib().experts_gather(x.data_ptr(), code, slots.data_ptr(), out.data_ptr(), T, top_k, H, s),
-               "experts_gather")
+        out, f = xs, lib().experts_gather
+        if xs is None:
+            out, f = torch.empty((T * top_k, H), dtype=x.dtype, device=x.device), lib().experts_gather_zero
+        _check(f(x.data_ptr(), code, slots.data_ptr(), out.data_ptr(), T, top_k, H, s), "experts_gather")
         return out
     return _run(x, stream, call)
 
@@ -662,7 +667,8 @@ def experts_combine(ys: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor
 def experts_combine_grad(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, dys=None,
                          dweights=None, stream=None):
     """Gradients of experts_combine: (dys [T * top_k, H] of ys's type, dweights [T, top_k] float32).
-    Rows of dys that no choice has are not written."""
+    Rows of dys that no choice has are not written in a dys that is given, zeros -- their gradient --
+    in one allocated here."""
     dy_code, ys_code = _float(dy, "dy"), _float(ys, "ys")
     T, top_k = _slots(slots, ys)
     H = ys.shape[1]
@@ -675,10 +681,11 @@ def experts_combine_grad(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor
         _is(dweights, torch.float32, (T, top_k), "dweights", ys)
 
     def call(s):
-        d = torch.empty((T * top_k, H), dtype=ys.dtype, device=ys.device) if dys is None else dys
+        d, f = dys, lib().experts_combine_grad
+        if dys is None:
+            d, f = torch.empty((T * top_k, H), dtype=ys.dtype, device=ys.device), lib().experts_combine_grad_zero
         dw = torch.empty((T, top_k), dtype=torch.float32, device=ys.device) if dweights is None else dweights
-        _check(lib().experts_combine_grad(dy.data_ptr(), dy_code, ys.data_ptr(), ys_code, slots.data_ptr(),
-                                          weights.data_ptr(), d.data_ptr(), dw.data_ptr(), T, top_k, H, s),
-               "experts_combine_grad")
+        _check(f(dy.data_ptr(), dy_code, ys.data_ptr(), ys_code, slots.data_ptr(), weights.data_ptr(), d.data_ptr(),
+                 dw.data_ptr(), T, top_k, H, s), "experts_combine_grad")
         return d, dw
     return _run(ys, stream, call)

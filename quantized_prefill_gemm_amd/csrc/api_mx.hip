@@ -52,6 +52,32 @@ int product(const void* w, const void* xm, void* y, int y_type, int64_t M, int64
     return status_of(qpg_launch_mmq_mxfp4(w, xm, y, y_type, M, N, K, s));
 }
 
+// zero: rows that no slot names become zeros, else they are left as they were.
+int gather(const void* x, int type, const int32_t* slots, void* xs, int64_t T, int64_t top_k, int64_t H, bool zero,
+           hipStream_t s)
+{
+    if (!x || !slots || !xs || !type_ok(type) || !slots_ok(T, top_k, H)) return QPG_EINVAL;
+    const uintptr_t a = qpg::type_bytes(type);
+    if (!aligned(x, a) || !aligned(xs, a) || !aligned(slots, 4)) return QPG_EALIGN;
+    const int rc = qpg_check_device();
+    if (rc != QPG_OK) return rc;
+    return status_of(qpg_launch_experts_gather(x, type, slots, xs, T, top_k, H, zero, s));
+}
+
+int combine_grad(const void* dy, int dy_type, const void* ys, int ys_type, const int32_t* slots, const float* weights,
+                 void* dys, float* dweights, int64_t T, int64_t top_k, int64_t H, bool zero, hipStream_t s)
+{
+    if (!dy || !ys || !slots || !weights || !dys || !dweights) return QPG_EINVAL;
+    if (!type_ok(dy_type) || !type_ok(ys_type) || !slots_ok(T, top_k, H)) return QPG_EINVAL;
+    if (!aligned(dy, qpg::type_bytes(dy_type)) || !aligned(ys, qpg::type_bytes(ys_type)) ||
+        !aligned(dys, qpg::type_bytes(ys_type)) || !aligned(slots, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+        return QPG_EALIGN;
+    const int rc = qpg_check_device();
+    if (rc != QPG_OK) return rc;
+    return status_of(qpg_launch_experts_combine_grad(dy, dy_type, ys, ys_type, slots, weights, dys, dweights, T, top_k,
+                                                     H, zero, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -143,12 +169,13 @@ int mmq_mxfp4_experts(const void* w, const void* xm, int64_t rows, const int32_t
 int experts_gather(const void* x, int type, const int32_t* slots, void* xs, int64_t T, int64_t top_k, int64_t H,
                    qpg_stream_t stream)
 {
-    if (!x || !slots || !xs || !type_ok(type) || !slots_ok(T, top_k, H)) return QPG_EINVAL;
-    const uintptr_t a = qpg::type_bytes(type);
-    if (!aligned(x, a) || !aligned(xs, a) || !aligned(slots, 4)) return QPG_EALIGN;
-    const int rc = qpg_check_device();
-    if (rc != QPG_OK) return rc;
-    return status_of(qpg_launch_experts_gather(x, type, slots, xs, T, top_k, H, reinterpret_cast<hipStream_t>(stream)));
+    return gather(x, type, slots, xs, T, top_k, H, false, reinterpret_cast<hipStream_t>(stream));
+}
+
+int experts_gather_zero(const void* x, int type, const int32_t* slots, void* xs, int64_t T, int64_t top_k, int64_t H,
+                        qpg_stream_t stream)
+{
+    return gather(x, type, slots, xs, T, top_k, H, true, reinterpret_cast<hipStream_t>(stream));
 }
 
 int experts_combine(const void* ys, int ys_type, const int32_t* slots, const float* weights, void* y, int y_type,
@@ -168,15 +195,16 @@ int experts_combine_grad(const void* dy, int dy_type, const void* ys, int ys_typ
                          const float* weights, void* dys, float* dweights, int64_t T, int64_t top_k, int64_t H,
                          qpg_stream_t stream)
 {
-    if (!dy || !ys || !slots || !weights || !dys || !dweights) return QPG_EINVAL;
-    if (!type_ok(dy_type) || !type_ok(ys_type) || !slots_ok(T, top_k, H)) return QPG_EINVAL;
-    if (!aligned(dy, qpg::type_bytes(dy_type)) || !aligned(ys, qpg::type_bytes(ys_type)) ||
-        !aligned(dys, qpg::type_bytes(ys_type)) || !aligned(slots, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
-        return QPG_EALIGN;
-    const int rc = qpg_check_device();
-    if (rc != QPG_OK) return rc;
-    return status_of(qpg_launch_experts_combine_grad(dy, dy_type, ys, ys_type, slots, weights, dys, dweights, T, top_k,
-                                                     H, reinterpret_cast<hipStream_t>(stream)));
+    return combine_grad(dy, dy_type, ys, ys_type, slots, weights, dys, dweights, T, top_k, H, false,
+                        reinterpret_cast<hipStream_t>(stream));
+}
+
+int experts_combine_grad_zero(const void* dy, int dy_type, const void* ys, int ys_type, const int32_t* slots,
+                              const float* weights, void* dys, float* dweights, int64_t T, int64_t top_k, int64_t H,
+                              qpg_stream_t stream)
+{
+    return combine_grad(dy, dy_type, ys, ys_type, slots, weights, dys, dweights, T, top_k, H, true,
+                        reinterpret_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -213,11 +213,11 @@ struct Item {
     int64_t t;
     int64_t seg;
 };
-__device__ __forceinline__ Item wave_item(int per_block)
+__device__ __forceinline__ Item wave_item(unsigned block, int per_block)
 {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int shift = per_block >> 1;                 // log2 of 1, 2, 4
-    return {(int64_t)blockIdx.x * (4 >> shift) + (wave >> shift), (int64_t)blockIdx.y * per_block + (wave & (per_block - 1))};
+    return {(int64_t)block * (4 >> shift) + (wave >> shift), (int64_t)blockIdx.y * per_block + (wave & (per_block - 1))};
 }
 
 struct Grid {
@@ -232,18 +232,88 @@ inline Grid grid_of(int64_t tokens, int64_t H, int segment)
     return {dim3((unsigned)((tokens * per + 3) / 4), (unsigned)(y < 65535 ? y : 65535)), per};
 }
 
+// Rows that no slot names become zeros where the caller asks for it: the launch then starts with
+// zero_blocks(S) workgroups that take ZERO_ROWS of the S rows each, mark in LDS those that any
+// slot names and zero the others, beside the workgroups that write the named ones. Each reads all
+// slots, S^2 / ZERO_ROWS reads, where zeroing all rows in a launch of its own writes S rows; so the
+// one or the other by slots to bytes of a row, and up to 8192 slots, which are read faster than
+// a launch is made, always the first. Gather in us, zeroed beside / by itself / not at all: 32768
+// slots of 8 KB 53.5 / 87 / 53.3, 2^17 of 256 bytes 36.6 / 25.6 / 19, of 2 KB 59 / 87 / 53.5, 2^18 of
+// 256 bytes 87 / 44 / 34, of 2 KB 114 / 191 / 106, of 8 KB 416 / 841 / 422, 2^19 of 2 KB 327 / 405 / 209 (and
+// the gradients of the weighted sum there 675 / 652 / 457).
+constexpr int ZERO_ROWS = 256, ZERO_UNROLL = 16;
+
+inline bool zero_beside(int64_t S, int64_t row_bytes)
+{
+    return S <= 8192 || (S <= 128 * row_bytes && S <= (int64_t)1 << 22);      // S / 256 more workgroups: launchable
+}
+
+inline unsigned zero_blocks(int64_t S) { return (unsigned)((S + ZERO_ROWS - 1) / ZERO_ROWS); }
+
+template <typename T, int VEC>
+__device__ __forceinline__ void zero_unnamed(unsigned block, const int32_t* __restrict__ slots, int S, T* __restrict__ rows,
+                                             int64_t H)
+{
+    __shared__ uint32_t named[ZERO_ROWS / 32];
+    const int tid = threadIdx.x, first = (int)block * ZERO_ROWS;
+    if (tid < ZERO_ROWS / 32) named[tid] = 0;
+    __syncthreads();
+    for (int i0 = tid; i0 < S; i0 += 256 * ZERO_UNROLL) {
+        int32_t r[ZERO_UNROLL];
+#pragma unroll
+        for (int u = 0; u < ZERO_UNROLL; ++u) r[u] = slots[min(i0 + 256 * u, S - 1)];      // past the last: the last again
+#pragma unroll
+        for (int u = 0; u < ZERO_UNROLL; ++u) {
+            const unsigned d = (unsigned)r[u] - (unsigned)first;
+            if (d < ZERO_ROWS) atomicOr(&named[d >> 5], 1u << (d & 31));
+        }
+    }
+    __syncthreads();
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    for (int q = wave; q < ZERO_ROWS / 32; q += 4) {
+        const int row0 = first + 32 * q;
+        uint32_t left = ~(uint32_t)__builtin_amdgcn_readfirstlane((int)named[q]);
+        if (S - row0 < 32) left &= S > row0 ? (1u << (S - row0)) - 1 : 0u;
+        for (; left; left &= left - 1) {
+            const __amdgpu_buffer_rsrc_t to = row_of(rows, row0 + __builtin_ctz(left), H, sizeof(T));
+            for (int64_t h0 = (int64_t)blockIdx.y * 64 * VEC; h0 < H; h0 += (int64_t)gridDim.y * 64 * VEC)
+                store_row<T, VEC>(to, (unsigned)h0 + (tid & 63) * VEC, Pack<T, VEC>{});
+        }
+    }
+}
+
+constexpr int ZERO_STORES = 4;
+
+template <typename V>
+__global__ void __launch_bounds__(256) zero_kernel(V* __restrict__ p, int64_t n)
+{
+    constexpr int PART = 256 * ZERO_STORES;
+    for (int64_t at = (int64_t)blockIdx.x * PART; at < n; at += (int64_t)gridDim.x * PART) {
+#pragma unroll
+        for (int u = 0; u < ZERO_STORES; ++u) {
+            const int64_t i = at + 256 * u + threadIdx.x;
+            if (i < n) p[i] = V{};
+        }
+    }
+}
+
 constexpr int GATHER_UNROLL = 4;
 
 // xs[slots[t][j]] = x[t]: a wave reads its segment of a token once and writes it top_k times
 // (8192 tokens of 8 KB to 4 rows each: 336 MB in 64 us, 5.3 TB/s, what a large copy reaches).
 // T here is only a width: the values are moved, not read.
-template <typename T, int VEC>
+template <typename T, int VEC, bool ZERO>
 __global__ void __launch_bounds__(256) gather_kernel(const T* __restrict__ x, const int32_t* __restrict__ slots,
                                                      T* __restrict__ xs, int64_t tokens, int top_k, int64_t H,
-                                                     int per_block)
+                                                     int per_block, unsigned zeroing)
 {
     constexpr int SEG = 64 * VEC * GATHER_UNROLL;
-    const Item it = wave_item(per_block);
+    unsigned block = blockIdx.x;
+    if constexpr (ZERO) {
+        if (block < zeroing) return zero_unnamed<T, VEC>(block, slots, (int)(tokens * top_k), xs, H);
+        block -= zeroing;
+    }
+    const Item it = wave_item(block, per_block);
     if (it.t >= tokens) return;
     const __amdgpu_buffer_rsrc_t from = row_of(x, it.t, H, sizeof(T));
     for (int64_t s0 = it.seg * SEG; s0 < H; s0 += (int64_t)gridDim.y * per_block * SEG) {
@@ -271,7 +341,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const TI* __restrict__ ys,
                                                       int64_t tokens, int top_k, int64_t H, int per_block)
 {
     constexpr int U = COMBINE_UNROLL, J = COMBINE_SLOTS, SEG = 64 * VEC * U;
-    const Item it = wave_item(per_block);
+    const Item it = wave_item(blockIdx.x, per_block);
     if (it.t >= tokens) return;
     const __amdgpu_buffer_rsrc_t to = row_of(y, it.t, H, sizeof(TO));
     for (int64_t s0 = it.seg * SEG; s0 < H; s0 += (int64_t)gridDim.y * per_block * SEG) {
@@ -330,15 +400,20 @@ __device__ __forceinline__ float wave_sum64(float v)
 // 8 KB, 570 MB in 94 us (6.1 TB/s).
 constexpr int GRAD_SLOTS = 8;
 
-template <typename TI, typename TO, int VEC>
+template <typename TI, typename TO, int VEC, bool ZERO>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const TO* __restrict__ dy, const TI* __restrict__ ys,
                                                            const int32_t* __restrict__ slots,
                                                            const float* __restrict__ weights, TI* __restrict__ dys,
                                                            float* __restrict__ dweights, int64_t tokens, int top_k,
-                                                           int64_t H)
+                                                           int64_t H, unsigned zeroing)
 {
     __shared__ float part[4][GRAD_SLOTS];
-    const int64_t t = blockIdx.x;
+    unsigned block = blockIdx.x;
+    if constexpr (ZERO) {
+        if (block < zeroing) return zero_unnamed<TI, VEC>(block, slots, (int)(tokens * top_k), dys, H);
+        block -= zeroing;
+    }
+    const int64_t t = block;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const __amdgpu_buffer_rsrc_t dy_row = row_of(dy, t, H, sizeof(TO));
     for (int j0 = 0; j0 < top_k; j0 += GRAD_SLOTS) {
@@ -394,6 +469,22 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const TO* __restrict_
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
+// All rows zeroed, ahead of a launch whose workgroups would have too many slots to read.
+template <typename V>
+hipError_t launch_zero_as(void* p, int64_t bytes, hipStream_t s)
+{
+    const int64_t n = bytes / (int64_t)sizeof(V), blocks = (n + 256 * ZERO_STORES - 1) / (256 * ZERO_STORES);
+    hipLaunchKernelGGL(zero_kernel<V>, dim3((unsigned)(blocks < 1 << 22 ? blocks : 1 << 22)), dim3(256), 0, s,
+                       static_cast<V*>(p), n);
+    return hipGetLastError();
+}
+
+inline hipError_t launch_zero(void* p, int64_t bytes, hipStream_t s)
+{
+    if (aligned16(p) && bytes % 16 == 0) return launch_zero_as<uint32x4>(p, bytes, s);
+    return launch_zero_as<uint16_t>(p, bytes, s);
+}
+
 template <typename F>
 hipError_t by_types(int a, int b, F f)
 {
@@ -423,18 +514,26 @@ hipError_t qpg_launch_experts_sort(const void* ids, int id_bytes, int64_t S, int
 }
 
 hipError_t qpg_launch_experts_gather(const void* x, int type, const int32_t* slots, void* xs, int64_t T, int64_t top_k,
-                                     int64_t H, hipStream_t s)
+                                     int64_t H, bool zero, hipStream_t s)
 {
+    const int64_t row = H * (int64_t)qpg::type_bytes(type);
+    if (zero && !qpg::zero_beside(T * top_k, row)) {
+        const hipError_t rc = qpg::launch_zero(xs, T * top_k * row, s);
+        if (rc != hipSuccess) return rc;
+        zero = false;
+    }
     auto go = [&](auto unit, auto vec) {
         typedef decltype(unit) U;
         constexpr int VEC = decltype(vec)::value;
-        const int64_t n = H * (int64_t)qpg::type_bytes(type) / (int64_t)sizeof(U);
-        const qpg::Grid g = qpg::grid_of(T, n, 64 * VEC * qpg::GATHER_UNROLL);
-        hipLaunchKernelGGL((qpg::gather_kernel<U, VEC>), g.blocks, dim3(256), 0, s, static_cast<const U*>(x), slots,
-                           static_cast<U*>(xs), T, (int)top_k, n, g.per_block);
+        const int64_t n = row / (int64_t)sizeof(U);
+        qpg::Grid g = qpg::grid_of(T, n, 64 * VEC * qpg::GATHER_UNROLL);
+        const unsigned zeroing = zero ? qpg::zero_blocks(T * top_k) : 0;
+        g.blocks.x += zeroing;
+        auto kernel = zero ? qpg::gather_kernel<U, VEC, true> : qpg::gather_kernel<U, VEC, false>;
+        hipLaunchKernelGGL(kernel, g.blocks, dim3(256), 0, s, static_cast<const U*>(x), slots, static_cast<U*>(xs), T,
+                           (int)top_k, n, g.per_block, zeroing);
         return hipGetLastError();
     };
-    const int64_t row = H * (int64_t)qpg::type_bytes(type);
     if (row % 16 == 0 && qpg::aligned16(x) && qpg::aligned16(xs)) return go(uint32_t(), std::integral_constant<int, 4>());
     if (type == QPG_F32) return go(uint32_t(), std::integral_constant<int, 1>());
     return go(uint16_t(), std::integral_constant<int, 1>());
@@ -462,16 +561,24 @@ hipError_t qpg_launch_experts_combine(const void* ys, int ys_type, const int32_t
 
 hipError_t qpg_launch_experts_combine_grad(const void* dy, int dy_type, const void* ys, int ys_type,
                                            const int32_t* slots, const float* weights, void* dys, float* dweights,
-                                           int64_t T, int64_t top_k, int64_t H, hipStream_t s)
+                                           int64_t T, int64_t top_k, int64_t H, bool zero, hipStream_t s)
 {
+    const int64_t row = H * (int64_t)qpg::type_bytes(ys_type);
+    if (zero && !qpg::zero_beside(T * top_k, row)) {
+        const hipError_t rc = qpg::launch_zero(dys, T * top_k * row, s);
+        if (rc != hipSuccess) return rc;
+        zero = false;
+    }
+    const unsigned zeroing = zero ? qpg::zero_blocks(T * top_k) : 0;
     return qpg::by_types(ys_type, dy_type, [&](auto ti, auto to) {
         typedef typename qpg::Store<decltype(ti)::value>::type TI;
         typedef typename qpg::Store<decltype(to)::value>::type TO;
         auto go = [&](auto vec) {
             constexpr int VEC = decltype(vec)::value;
-            hipLaunchKernelGGL((qpg::combine_grad_kernel<TI, TO, VEC>), dim3((unsigned)T), dim3(256), 0, s,
-                               static_cast<const TO*>(dy), static_cast<const TI*>(ys), slots, weights,
-                               static_cast<TI*>(dys), dweights, T, (int)top_k, H);
+            auto kernel = zero ? qpg::combine_grad_kernel<TI, TO, VEC, true> : qpg::combine_grad_kernel<TI, TO, VEC, false>;
+            hipLaunchKernelGGL(kernel, dim3((unsigned)T + zeroing), dim3(256), 0, s, static_cast<const TO*>(dy),
+                               static_cast<const TI*>(ys), slots, weights, static_cast<TI*>(dys), dweights, T, (int)top_k, H,
+                               zeroing);
             return hipGetLastError();
         };
         constexpr int V = 16 / (sizeof(TI) > sizeof(TO) ? sizeof(TI) : sizeof(TO));

@@ -102,9 +102,9 @@ int qpg_experts_sort_blocks(int64_t S);
 hipError_t qpg_launch_experts_sort(const void* ids, int id_bytes, int64_t S, int64_t E, int32_t* offsets,
                                    int32_t* order, int32_t* slots, void* ws, hipStream_t s);
 hipError_t qpg_launch_experts_gather(const void* x, int type, const int32_t* slots, void* xs, int64_t T, int64_t top_k,
-                                     int64_t H, hipStream_t s);
+                                     int64_t H, bool zero, hipStream_t s);
 hipError_t qpg_launch_experts_combine(const void* ys, int ys_type, const int32_t* slots, const float* weights, void* y,
                                       int y_type, int64_t T, int64_t top_k, int64_t H, hipStream_t s);
 hipError_t qpg_launch_experts_combine_grad(const void* dy, int dy_type, const void* ys, int ys_type,
                                            const int32_t* slots, const float* weights, void* dys, float* dweights,
-                                           int64_t T, int64_t top_k, int64_t H, hipStream_t s);
+                                           int64_t T, int64_t top_k, int64_t H, bool zero, hipStream_t s);
