@@ -139,6 +139,8 @@ class ExpertStack(Stack):
             raise ValueError(f"{len(weights)} layers of projections, {len(experts)} of experts")
         if not 1 <= top_k <= E:
             raise ValueError(f"{top_k} choices of {E} experts")
+        if q6 not in ("raw", "prepared", "expanded"):
+            raise ValueError(f"q6 form {q6!r}")
         self.M, self.E, self.top_k, self.S = M, E, top_k, M * top_k
         self.q6, self.per_layer, self.L = q6, per_layer, len(weights)
         dev = weights[0][0].device
