@@ -236,16 +236,16 @@ inline Grid grid_of(int64_t tokens, int64_t H, int segment)
 // zero_blocks(S) workgroups that take ZERO_ROWS of the S rows each, mark in LDS those that any
 // slot names and zero the others, beside the workgroups that write the named ones. Each reads all
 // slots, S^2 / ZERO_ROWS reads, where zeroing all rows in a launch of its own writes S rows; so the
-// one or the other by slots to bytes of a row, and up to 8192 slots, which are read faster than
-// a launch is made, always the first. Gather in us, zeroed beside / by itself / not at all: 32768
-// slots of 8 KB 53.5 / 87 / 53.3, 2^17 of 256 bytes 36.6 / 25.6 / 19, of 2 KB 59 / 87 / 53.5, 2^18 of
-// 256 bytes 87 / 44 / 34, of 2 KB 114 / 191 / 106, of 8 KB 416 / 841 / 422, 2^19 of 2 KB 327 / 405 / 209 (and
-// the gradients of the weighted sum there 675 / 652 / 457).
+// one or the other by slots to bytes of a row, and up to 2^14 slots, which are read faster than
+// a launch is made, always the first. Gather in us, zeroed beside / by itself / not at all: 2^14
+// slots of 32 bytes 8.8 / 11.9 / 7.2, 2^17 of 256 bytes 33 / 26 / 20, of 2 KB 54 / 87 / 54, 2^18 of 256 bytes
+// 82 / 44 / 34, of 2 KB 111 / 191 / 106, of 8 KB 418 / 840 / 423, 2^19 of 2 KB 323 / 403 / 208 (and the
+// gradients of the weighted sum there 673 / 653 / 460).
 constexpr int ZERO_ROWS = 256, ZERO_UNROLL = 16;
 
 inline bool zero_beside(int64_t S, int64_t row_bytes)
 {
-    return S <= 8192 || (S <= 128 * row_bytes && S <= (int64_t)1 << 22);      // S / 256 more workgroups: launchable
+    return S <= 1 << 14 || (S <= 128 * row_bytes && S <= (int64_t)1 << 22);      // S / 256 more workgroups: launchable
 }
 
 inline unsigned zero_blocks(int64_t S) { return (unsigned)((S + ZERO_ROWS - 1) / ZERO_ROWS); }

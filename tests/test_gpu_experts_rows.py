@@ -14,10 +14,10 @@ from quantized_prefill_gemm_amd import binding as B
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
 KINDS = {"float32": torch.float32, "float16": torch.float16, "bfloat16": torch.bfloat16}
-# T, top_k, H, E: single and odd rows, rows of several segments, and from 8192 choices on rows that are
+# T, top_k, H, E: single and odd rows, rows of several segments, and from 2^14 choices on rows that are
 # zeroed beside the others (long ones) and ahead of them (short ones)
 CASES = [(1, 1, 1, 3), (7, 3, 33, 5), (130, 8, 1032, 16), (2100, 2, 520, 9), (5, 2, 20_001, 4), (9, 300, 17_000, 4),
-         (4096, 2, 3, 9), (4097, 2, 3, 9), (2500, 4, 17, 6), (20_000, 4, 1000, 33), (65_537, 2, 40, 9), (43_691, 3, 17, 200)]
+         (8192, 2, 3, 9), (8193, 2, 3, 9), (5000, 4, 17, 6), (20_000, 4, 1000, 33), (65_537, 2, 40, 9), (43_691, 3, 17, 200)]
 
 
 def routing(T, top_k, E, rng):
