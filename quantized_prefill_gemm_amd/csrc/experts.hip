@@ -157,7 +157,9 @@ hipError_t launch_sort(const ID* ids, int64_t S, int E, int32_t* offsets, int32_
 // end reads zeros and writes nothing, and a slot without a row has an empty one. So there is
 // no branch around an access, and all loads of a wave are under way together (with branches the
 // compiler waits for each: the weighted sum of 268 MB took 84 us). VEC values per access: 16
-// bytes of the wider type where H and the pointers allow, else 1.
+// bytes of the wider type where H and the pointers allow, else 1 (4096 x 4 rows in us, gather /
+// weighted sum / its gradients: of 8192 bytes f16 27 / 27 / 49, of 8196 67 / 48 / 91; of 16384 bytes f32 54 / 51 /
+// 116, of 16388 93 / 51 / 174).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void* p, int64_t row, int64_t H, int bytes)
 {
     const char* at = static_cast<const char*>(p) + (row < 0 ? 0 : row * H * bytes);
@@ -181,8 +183,6 @@ __device__ __forceinline__ Pack<T, VEC> load_row(__amdgpu_buffer_rsrc_t r, unsig
 // Stores are non-temporal: the rows are not read again here, and ordinary ones push the rows
 // being read out of the caches (gather and gradient, 8192 x 4 rows of 8 KB: 158 -> 138 us; weighted
 // sum and gradients, 4096 x 8: 177 -> 149 us. Non-temporal loads as well: 135 and 161 us).
-constexpr int NONTEMPORAL = 2;
-
 template <typename T, int VEC>
 __device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, unsigned h, const Pack<T, VEC>& v)
 {
@@ -493,9 +493,12 @@ hipError_t by_types(int a, int b, F f)
 
 }  // namespace qpg
 
-// Blocks of the sort: one up to 4096 slots (a single launch, 7.3 us; 16 blocks 6.3), beyond 16,
-// doubled while a block has more than 1024 slots, at most 128 (each reads all blocks' counts).
-// With 128 experts: 8192 slots 6.5 us (one block 11.5), 32768 7.2 us (8 blocks 11.9), 2^20 18.5 us.
+// Blocks of the sort: one up to 4096 slots, a single launch, which is worth more to a call from the
+// host (4096 slots, 128 experts 7.3 us, 16 blocks 9.9) than it costs at the upper end of a graph
+// (7.1 against 6.0; 2048 slots, 8 experts 4.3 against 5.3). Beyond 16, doubled while a block has
+// more than 1024 slots, at most 128 (each reads all blocks' counts). With 128 experts, a call among
+// others in a graph: 8192 slots 6.3 us (one block 11.5), 32768 7.1 us (8 blocks 11.9), 2^20 19.8
+// us (a trace gives each of the two kernels its own start: 32768 slots 4.7 and 5.0 us).
 int qpg_experts_sort_blocks(int64_t S)
 {
     if (S <= 4096) return 1;
