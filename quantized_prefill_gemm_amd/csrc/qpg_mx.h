@@ -16,7 +16,6 @@ typedef float floatx2 __attribute__((ext_vector_type(2)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-constexpr int MX_BLOCK = 32;          // values that share one scale byte
 constexpr int NONTEMPORAL = 2;        // a buffer store's bit for memory that is not read again soon
 
 // Storage type of a QPG_F32 / QPG_F16 / QPG_BF16 argument; conversions from f32 round to
