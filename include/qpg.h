@@ -239,7 +239,8 @@ int mmq_q6K_exp_q8_sk(const void* we, const void* xq, float* y, int64_t M, int64
  * value is QPG_EINVAL. Arithmetic and sums are f32; a result is rounded once, to nearest
  * even, when it is stored. Shapes of this section: 1 <= M, N < 2^31; 32 <= K <= 2^24,
  * K % 32 == 0 (K / 32 need not be even or a multiple of anything), rows*K <= 2^35 - 2^11 of
- * every operand; the number of tiles of 16 x 16 outputs must be < 2^31.
+ * every operand; the number of tiles of 16 x 16 outputs must be < 2^31. Outputs and workspaces must
+ * not overlap inputs.
  */
 enum { QPG_F32 = 0, QPG_F16 = 1, QPG_BF16 = 2 };
 
@@ -272,7 +273,7 @@ int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int
 
 /*
  * Experts: T tokens, top_k choices each; slot t*top_k + j is token t's j-th choice. S = T*top_k
- * slots, 1 <= S <= 2^30, 1 <= E <= 1024 experts. Outputs must not overlap inputs.
+ * slots, 1 <= S <= 2^30, 1 <= E <= 1024 experts.
  *
  * experts_sort: ids [S] (int32 or int64: id_bytes 4 or 8) -> the slots sorted by expert, stable.
  *   offsets int32 [E + 1]: rows [offsets[e], offsets[e + 1]) of the sorted order are expert e's;
@@ -285,7 +286,8 @@ int mmq_mxfp4(const void* w, const void* x, int x_type, void* y, int y_type, int
  * mmq_mxfp4_experts: y [S][N]; for each row p < offsets[E], of expert e,
  *   y[p] = xm[order[p] / top_k] x w[e]^T, or xm[p] x w[e]^T with order null (activations already
  *   in sorted order; then rows == S). w: MXFP4 of E*N rows, xm: MXFP4 of `rows` rows;
- *   E * ceil(S / 16) < 2^31. Rows of y from offsets[E] on are left as they were. offsets and order
+ *   E * ceil(S / 16) < 2^31. With 2^32 bytes of xm's codes or more the streaming form runs whatever
+ *   the shape. Rows of y from offsets[E] on are left as they were. offsets and order
  *   are read on the device: values outside their ranges are clamped to them, so a wrong array
  *   gives wrong rows, never an access outside the buffers.
  *

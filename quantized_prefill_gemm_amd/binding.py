@@ -380,6 +380,7 @@ def mmq_q6K_exp_q8_sk(we, xq, M, N, K, y=None, ws=None, stream=None):
 
 # ---- MXFP4 and experts. The tensors of a call lie on one device, which need not be the current
 # one. Outputs and workspaces that are not given are allocated on the stream the call runs on.
+# No call records an autograd graph, whatever its operands require: gradients are calls of their own.
 # A small call is bound by the host (a launch takes 3.7 us, torch.cuda.current_stream() 2.9, an
 # allocation 1.4), so the checks below are one comparison each where nothing is wrong.
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}      # QPG_F32, QPG_F16, QPG_BF16
