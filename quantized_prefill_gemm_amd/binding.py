@@ -445,11 +445,11 @@ def _mx_weights(w: torch.Tensor, rows: int, K: int, ref: torch.Tensor):
     """MXFP4 weights of rows x K values. The scales start where the codes of all rows end, so the
     buffer of a matrix of more rows is no buffer of its first ones: a size of a whole number of
     other rows is refused. (Bytes behind the matrix that make up no rows are let pass.)"""
-    if w.numel() == mxfp4_bytes(rows, K) and w.dtype is torch.uint8 and w.get_device() == ref.get_device() >= 0 \
-            and w.is_contiguous():
+    need = _mx_bytes(rows, K, "w")
+    if w.numel() == need and w.dtype is torch.uint8 and w.get_device() == ref.get_device() >= 0 and w.is_contiguous():
         return
     _mx(w, rows, K, "w", ref)
-    if w.numel() != mxfp4_bytes(rows, K) and w.numel() * 32 % (17 * K) == 0:
+    if w.numel() != need and w.numel() * 32 % (17 * K) == 0:
         raise QPGError(QPG_EINVAL, f"w is the size of {w.numel() * 32 // (17 * K)} x {K} MXFP4 values, not of {rows} x {K}")
 
 

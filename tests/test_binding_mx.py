@@ -81,6 +81,15 @@ def test_weights_of_another_number_of_rows(run, N, K):
     assert run(lambda: B.mmq_mxfp4_experts(u8(size(4 * N)), xm, 4, i32(4), i32(8), 2, 3, N, K)) == B.QPG_EINVAL
 
 
+def test_weights_of_an_unsupported_shape(run):
+    """An empty buffer has the size (0) that mxfp4_bytes gives for a shape it does not support."""
+    x, xm = Fake(4, 64), u8(B.mxfp4_bytes(4, 64))
+    for N in (0, -1, 2 ** 31):
+        assert run(lambda: B.mmq_mxfp4(u8(0), x, N)) == B.QPG_EINVAL
+        assert run(lambda: B.mmq_mxfp4_mx(u8(0), xm, 4, N, 64)) == B.QPG_EINVAL
+        assert run(lambda: B.mmq_mxfp4_experts(u8(0), xm, 4, i32(2), None, 1, 1, N, 64)) == B.QPG_EINVAL
+
+
 def test_order_of_another_number_of_choices(run):
     """order has rows * top_k entries: with another top_k, or xm of another number of tokens, rows
     would be taken from the wrong tokens."""
