@@ -322,6 +322,86 @@ int experts_combine_grad_zero(const void* dy, int dy_type, const void* ys, int y
                               const float* weights, void* dys, float* dweights, int64_t T, int64_t top_k, int64_t H,
                               qpg_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A paged cache of keys and values: appending to it, and attention over it.
+ *
+ *   qpg_cache: k and v, each [pages][heads][page][dim] of `type` (QPG_F16 or QPG_BF16). A (page, head)
+ *     block is contiguous; pages lie k_stride and v_stride elements apart (at least
+ *     heads * page * dim, a multiple of 8). page: 16, 32, 64, 128 or 256 tokens; dim: a multiple of 8,
+ *     8 .. 256. k and v 16-byte aligned.
+ *   qpg_batch: B sequences, T rows of new tokens. offsets int32 [B + 1]: rows [offsets[b], offsets[b + 1]) are
+ *     the new tokens of sequence b, its last; rows outside [offsets[0], offsets[B]) are in no sequence, and no
+ *     call writes their outputs. lens int32 [B]: its length, the new tokens among it. table int32
+ *     [B][width]: its pages; token j is in page table[b][j / page], place j % page. Two sequences may share
+ *     pages that neither appends to. New token i of n is token lens[b] - n + i; of more new tokens
+ *     than lens[b] says the first have no place (not appended; as queries they see nothing of a causal mask).
+ *     The arrays are read on the device, so a captured graph replays with other contents: offsets are clamped to
+ *     [0, T], lens to [0, width * page], entries of the table to [0, pages). An entry that no visible key needs may
+ *     hold anything.
+ *   1 <= B <= 2^20, 1 <= T < 2^24, 1 <= heads <= 4096, query heads a multiple of the cache's, T * query heads < 2^31,
+ *   and an attention's launch less than 2^24 workgroups (B * heads of the cache is at most that); 1 <= width, width * page <= 2^30, 1 <= pages < 2^31. Arrays aligned to their element. Outputs and workspaces must not overlap inputs.
+ */
+typedef struct qpg_cache {
+    void* k;
+    void* v;
+    int type;
+    int64_t pages, heads, page, dim, k_stride, v_stride;
+} qpg_cache;
+
+typedef struct qpg_batch {
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* offsets;
+    int64_t B, width, T;
+} qpg_batch;
+
+/*
+ * What makes a score of a query at position i and a key at position j:
+ *   s = scale * <q, k>;  cap > 0: s = cap * tanh(s / cap);  slopes (f32 [query heads] or null): s -= slopes[h] * |i - j|
+ * and which keys a query sees: j <= i and, with window > 0, i - j < window; with prefix (int32 [B] or null) also every
+ * j < prefix[b]. (prefix = lens: every query sees the whole sequence.) scale > 0, cap >= 0, both finite; window >= 0.
+ */
+typedef struct qpg_scores {
+    float scale, cap;
+    const float* slopes;
+    int64_t window;
+    const int32_t* prefix;
+} qpg_scores;
+
+/*
+ * cache_append: for every row t of a sequence, with its place p there and the position positions[t] (int32 [T], or
+ *   null: p): q and k are normed by head -- x * rsqrt(mean(x^2) + eps) * norm, with q_norm / k_norm f32 [dim] or
+ *   null: not normed -- and their first `rot` values rotated: pair i, turned by position * freqs[i] (f32 [rot / 2];
+ *   the angle is made in 64 bits), is values (2i, 2i + 1) with adjacent != 0, (i, i + rot / 2) without. Then q goes to
+ *   y [T][heads][dim] of the cache's type, k and v to place p of the cache. Arithmetic is f32, rounded once.
+ *   q [T][heads * dim], k and v [T][cache heads * dim] of `type`; rows lie q_stride, k_stride, v_stride elements
+ *   apart (slices of one product), any element alignment; aligned to 16 bytes (8 of 16-bit types) is faster. q and y
+ *   null with heads 0: keys and values alone. rot % 8 == 0, 0 <= rot <= dim, freqs null with rot 0. A token
+ *   without a place, or whose entry of the table is no page, is not appended. y 16-byte aligned.
+ * cache_attention: y [T][heads][dim] = softmax(s) v over the keys that a query sees; a query that sees none gets
+ *   zeros. q [T][heads][dim] of the cache's type, 16-byte aligned; query head h reads head h / (heads / cache heads) of
+ *   the cache. Key j's position is j. Keys and values that a row does not see do not touch it, whatever they hold.
+ *   Scores and sums are f32. The shares that multiply the values are rounded to the cache's type (half a
+ *   step each); with a y_type of more bits than that they are two (f16) or three (bf16) pieces, which
+ *   leave f32's own errors (and make NaN of an infinite value that a row sees).
+ * cache_attention_tree: the new tokens of a sequence are nodes of a tree of drafts. A node sees the tokens before the
+ *   new ones, and node m iff bit m % 64 of word m / 64 of its row of `tree` (int64 [T][words]) is set: its ancestors and itself.
+ *   positions int32 [T], 0 .. 2^30, are the nodes' (the length before plus the depth), for window and slopes;
+ *   nodes from 64 * words on are seen by none. 1 <= words <= 1024. prefix must be null.
+ *   ws: qpg_cache_attention_bytes(T, B, heads, cache heads, dim, width * page) bytes, 16-byte aligned
+ *   (null when 0); calls that share it must not overlap in time. One or two kernels are enqueued.
+ */
+int cache_append(const qpg_cache* cache, const qpg_batch* batch, const void* q, const void* k, const void* v, int type,
+                 int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t heads, const int32_t* positions,
+                 const float* freqs, int64_t rot, int adjacent, const float* q_norm, const float* k_norm, float eps,
+                 void* y, qpg_stream_t stream);
+size_t qpg_cache_attention_bytes(int64_t T, int64_t B, int64_t heads, int64_t cache_heads, int64_t dim, int64_t length);
+int cache_attention(const qpg_cache* cache, const qpg_batch* batch, const qpg_scores* scores, const void* q, int64_t heads,
+                    void* y, int y_type, void* ws, qpg_stream_t stream);
+int cache_attention_tree(const qpg_cache* cache, const qpg_batch* batch, const qpg_scores* scores, const void* q,
+                         int64_t heads, const int64_t* tree, int64_t words, const int32_t* positions, void* y, int y_type,
+                         void* ws, qpg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

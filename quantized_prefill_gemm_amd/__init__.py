@@ -12,7 +12,8 @@ __all__ = ["inputs", "q8_1_bytes", "quantize_q8_1", "mmq_q4K", "mmq_q6K", "mmq_q
            "mmq_sk_bytes", "mmq_q4K_q8_sk", "mmq_q6K_q8_sk", "mmq_q6K_prep_q8_sk", "mmq_q6K_exp_q8_sk",
            "mxfp4_bytes", "quantize_mxfp4", "dequantize_mxfp4", "mmq_mxfp4", "mmq_mxfp4_mx", "mmq_mxfp4_experts",
            "experts_sort", "experts_sort_bytes", "experts_gather", "experts_gather_grad", "experts_combine",
-           "experts_combine_grad", "QPGError"]
+           "experts_combine_grad", "cache_append", "cache_attention", "cache_attention_bytes", "cache_attention_tree",
+           "QPGError"]
 
 
 def __getattr__(name):

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -80,6 +81,12 @@ def lib() -> ctypes.CDLL:
                 (L.experts_combine_grad, INT, [P, INT, P, INT, P, P, P, P, I64, I64, I64, P]),
                 (L.experts_combine_grad_zero, INT, [P, INT, P, INT, P, P, P, P, I64, I64, I64, P])):
             f.restype, f.argtypes = res, args
+        F = ctypes.c_float
+        L.cache_append.restype = L.cache_attention.restype = L.cache_attention_tree.restype = INT
+        L.cache_append.argtypes = [P, P, P, P, P, INT, I64, I64, I64, I64, P, P, I64, INT, P, P, F, P, P]
+        L.cache_attention.argtypes = [P, P, P, P, I64, P, INT, P, P]
+        L.cache_attention_tree.argtypes = [P, P, P, P, I64, P, I64, P, P, INT, P, P]
+        L.qpg_cache_attention_bytes.restype, L.qpg_cache_attention_bytes.argtypes = SIZE, [I64] * 6
         _lib = L
     return _lib
 
@@ -91,7 +98,8 @@ EXPORTS = ("qpg_strerror", "qpg_q8_1_bytes", "quantize_q8_1", "mmq_q4K", "mmq_q6
            "mmq_q6K_exp_q8_sk", "mmq_q4K_noalloc", "qpg_mxfp4_bytes", "quantize_mxfp4", "dequantize_mxfp4",
            "mmq_mxfp4_mx", "mmq_mxfp4", "qpg_experts_sort_bytes", "experts_sort", "mmq_mxfp4_experts",
            "experts_gather", "experts_gather_zero", "experts_combine", "experts_combine_grad",
-           "experts_combine_grad_zero")
+           "experts_combine_grad_zero", "cache_append", "qpg_cache_attention_bytes", "cache_attention",
+           "cache_attention_tree")
 
 
 def _check(rc: int, what: str):
@@ -690,3 +698,203 @@ def experts_combine_grad(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor
                  dw.data_ptr(), T, top_k, H, s), "experts_combine_grad")
         return d, dw
     return _run(ys, stream, call)
+
+
+# ---- A paged cache of keys and values. As above: one device, outputs and workspaces allocated on the
+# stream where none are given, no autograd graph.
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("type", ctypes.c_int)] + \
+        [(n, ctypes.c_int64) for n in ("pages", "heads", "page", "dim", "k_stride", "v_stride")]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("table", "lens", "offsets")] + [(n, ctypes.c_int64) for n in ("B", "width", "T")]
+
+
+class _Scores(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("cap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("window", ctypes.c_int64),
+                ("prefix", ctypes.c_void_p)]
+
+
+def _cache(k: torch.Tensor, v: torch.Tensor):
+    """The cache as the library takes it: [pages, heads, page, dim] each, pages any distance apart."""
+    code = _TYPES.get(k.dtype, 0)
+    if code == 0:
+        raise QPGError(QPG_EINVAL, f"k_cache must be float16 or bfloat16, got {k.dtype}")
+    shape = k.shape
+    if len(shape) != 4:
+        raise QPGError(QPG_EINVAL, f"k_cache must have 4 dimensions, got {tuple(shape)}")
+    if min(shape) < 1:
+        raise QPGError(QPG_EINVAL, f"k_cache is empty: {tuple(shape)}")
+    pages, heads, page, dim = shape
+    for t, name in ((k, "k_cache"), (v, "v_cache")):
+        if t.dtype is not k.dtype or t.shape != shape or t.get_device() != k.get_device() or t.get_device() < 0:
+            if not t.is_cuda:
+                raise QPGError(QPG_EINVAL, f"{name} must be a device tensor")
+            _same_device(t, k, name)
+            raise QPGError(QPG_EINVAL, f"{name} must be {k.dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        s = t.stride()
+        # an extent of 1 has no stride to speak of
+        if (dim > 1 and s[3] != 1) or (page > 1 and s[2] != dim) or (heads > 1 and s[1] != page * dim) or \
+                (pages > 1 and s[0] < heads * page * dim):
+            raise QPGError(QPG_EINVAL, f"{name} must be contiguous within a page, strides {s}")
+    block = heads * page * dim
+    return _Cache(k.data_ptr(), v.data_ptr(), code, pages, heads, page, dim, k.stride(0) if pages > 1 else block,
+                  v.stride(0) if pages > 1 else block)
+
+
+def _batch(table: torch.Tensor, lens: torch.Tensor, offsets: torch.Tensor, T: int, ref: torch.Tensor):
+    if table.dim() != 2:
+        raise QPGError(QPG_EINVAL, f"table must have 2 dimensions, got {tuple(table.shape)}")
+    B, width = table.shape
+    _is(table, torch.int32, (B, width), "table", ref)
+    _is(lens, torch.int32, (B,), "lens", ref)
+    _is(offsets, torch.int32, (B + 1,), "offsets", ref)
+    return _Batch(table.data_ptr(), lens.data_ptr(), offsets.data_ptr(), B, width, T)
+
+
+def _at(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _heads(t: torch.Tensor, dim: int, name: str, ref: torch.Tensor) -> int:
+    """Heads of a matrix [T, heads * dim] whose rows are contiguous, any distance apart."""
+    if t.get_device() != ref.get_device():
+        if not t.is_cuda:
+            raise QPGError(QPG_EINVAL, f"{name} must be a device tensor")
+        _same_device(t, ref, name)
+    if t.dim() != 2:
+        raise QPGError(QPG_EINVAL, f"{name} must have 2 dimensions, got {tuple(t.shape)}")
+    T, n = t.shape
+    if n % dim:
+        raise QPGError(QPG_EINVAL, f"{name}: rows of {n} are no heads of {dim}")
+    if (n > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < n):
+        raise QPGError(QPG_EINVAL, f"{name} must have contiguous rows, strides {t.stride()}")
+    return n // dim
+
+
+def cache_append(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                 lens: torch.Tensor, offsets: torch.Tensor, freqs=None, positions=None, adjacent: bool = False, q_norm=None,
+                 k_norm=None, eps: float = 1e-6, y=None, stream=None):
+    """Append the new tokens' keys and values to a paged cache, normed by head and rotated on the way,
+    and return the queries likewise: y [T, heads, dim] of the cache's type (None without q).
+
+    q [T, heads * dim], k, v [T, cache heads * dim]: float32, float16 or bfloat16, rows any distance apart (slices of one product).
+    k_cache, v_cache [pages, cache heads, page, dim], float16 or bfloat16; table [B, width], lens [B] (with the
+    new tokens), offsets [B + 1], int32: rows offsets[b] .. offsets[b + 1] are the last tokens of sequence b; rows outside are
+    left alone. freqs [rot / 2] float32: a pair of values turns by position * freq (None: no rotation); pairs are
+    neighbours (adjacent) or half a rotation apart. positions [T] int32 (None: the place in the sequence).
+    q_norm, k_norm [dim] float32: weights of the norm (None: none)."""
+    shape = k_cache.shape
+    cache = _cache(k_cache, v_cache)
+    dim, code = cache.dim, _type(k.dtype, "k")
+    heads = 0
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t is None and name == "q":
+            continue
+        n = _heads(t, dim, name, k_cache)
+        if t.dtype is not k.dtype or t.shape[0] != k.shape[0]:
+            raise QPGError(QPG_EINVAL, f"{name} is {t.dtype} of {t.shape[0]} rows, k {k.dtype} of {k.shape[0]}")
+        if name == "q":
+            heads = n
+            if n < 1 or n % shape[1]:
+                raise QPGError(QPG_EINVAL, f"{n} query heads over {shape[1]} heads of the cache")
+        elif n != shape[1]:
+            raise QPGError(QPG_EINVAL, f"{name} has {n} heads, the cache {shape[1]}")
+    T = k.shape[0]
+    batch = _batch(table, lens, offsets, T, k_cache)
+    rot = 0
+    if freqs is not None:
+        rot = 2 * freqs.numel()
+        _is(freqs, torch.float32, (rot // 2,), "freqs", k_cache)
+    if positions is not None:
+        _is(positions, torch.int32, (T,), "positions", k_cache)
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None:
+            _is(t, torch.float32, (dim,), name, k_cache)
+    if y is not None:
+        if q is None:
+            raise QPGError(QPG_EINVAL, "y without q")
+        _is(y, k_cache.dtype, (T, heads, dim), "y", k_cache)
+
+    def call(s):
+        out = y
+        if y is None and heads:
+            out = torch.empty((T, heads, dim), dtype=k_cache.dtype, device=k_cache.device)
+        _check(lib().cache_append(ctypes.byref(cache), ctypes.byref(batch), _at(q), k.data_ptr(), v.data_ptr(), code,
+                                  0 if q is None else q.stride(0), k.stride(0), v.stride(0), heads, _at(positions), _at(freqs),
+                                  rot, bool(adjacent), _at(q_norm), _at(k_norm), eps, _at(out), s), "cache_append")
+        return out
+    return _run(k_cache, stream, call)
+
+
+@functools.lru_cache(maxsize=4096)
+def cache_attention_bytes(T: int, B: int, heads: int, cache_heads: int, dim: int, length: int) -> int:
+    """Bytes of the attentions' workspace for tables of `length` = width * page tokens (0: none, or an unsupported shape)."""
+    return int(lib().qpg_cache_attention_bytes(T, B, heads, cache_heads, dim, length))
+
+
+def _attention(q, k_cache, v_cache, table, lens, offsets, scale, cap, slopes, window, prefix, tree, positions, y, ws, dtype,
+               stream, what):
+    cache = _cache(k_cache, v_cache)
+    if q.dim() != 3:
+        raise QPGError(QPG_EINVAL, f"q must have 3 dimensions, got {tuple(q.shape)}")
+    T, heads, dim = q.shape
+    if dim != cache.dim or heads < 1 or heads % cache.heads:
+        raise QPGError(QPG_EINVAL, f"{heads} query heads of {dim} over {cache.heads} heads of {cache.dim}")
+    _is(q, k_cache.dtype, (T, heads, dim), "q", k_cache)
+    batch = _batch(table, lens, offsets, T, k_cache)
+    if slopes is not None:
+        _is(slopes, torch.float32, (heads,), "slopes", k_cache)
+    if prefix is not None:
+        _is(prefix, torch.int32, (batch.B,), "prefix", k_cache)
+    words = 0
+    if tree is not None:
+        if tree.dim() != 2:
+            raise QPGError(QPG_EINVAL, f"tree must have 2 dimensions, got {tuple(tree.shape)}")
+        words = tree.shape[1]
+        _is(tree, torch.int64, (T, words), "tree", k_cache)
+        _is(positions, torch.int32, (T,), "positions", k_cache)
+    dtype, code = _given(y, q.dtype if dtype is None else dtype, (T, heads, dim), "y", k_cache)
+    nws = cache_attention_bytes(T, batch.B, heads, cache.heads, dim, batch.width * cache.page)
+    if ws is not None:
+        _out(ws, torch.uint8, "ws", nws, k_cache)
+    scores = _Scores(1.0 / math.sqrt(dim) if scale is None else scale, cap, _at(slopes), window, _at(prefix))
+
+    def call(s):
+        out = torch.empty((T, heads, dim), dtype=dtype, device=q.device) if y is None else y
+        w = torch.empty(nws, dtype=torch.uint8, device=q.device) if ws is None and nws else ws
+        args = ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(scores), q.data_ptr(), heads
+        if tree is None:
+            rc = lib().cache_attention(*args, out.data_ptr(), code, _at(w), s)
+        else:
+            rc = lib().cache_attention_tree(*args, tree.data_ptr(), words, positions.data_ptr(), out.data_ptr(), code, _at(w), s)
+        _check(rc, what)
+        return out
+    return _run(k_cache, stream, call)
+
+
+def cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                    offsets: torch.Tensor, scale=None, cap: float = 0.0, slopes=None, window: int = 0, prefix=None, y=None,
+                    ws=None, dtype=None, stream=None) -> torch.Tensor:
+    """y [T, heads, dim]: attention of the new tokens' queries q [T, heads, dim] (as cache_append gives them) over
+    the cache, which holds their own keys already. Query heads share the cache's heads in groups of neighbours.
+    A token sees the keys up to its own; with window > 0 of those the last `window`; with prefix [B] int32
+    also all keys before prefix[b] (prefix = lens: the whole sequence). Scores: scale (1 / sqrt(dim)) times the
+    product, cap > 0: cap * tanh(score / cap), slopes [heads] float32: minus slope times the distance. Rows that see
+    no key are zeros, rows of no sequence left alone. dtype: y's (q's if neither is given); ws:
+    cache_attention_bytes(...) bytes of uint8."""
+    return _attention(q, k_cache, v_cache, table, lens, offsets, scale, cap, slopes, window, prefix, None, None, y, ws, dtype,
+                      stream, "cache_attention")
+
+
+def cache_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                         lens: torch.Tensor, offsets: torch.Tensor, tree: torch.Tensor, positions: torch.Tensor, scale=None,
+                         cap: float = 0.0, slopes=None, window: int = 0, y=None, ws=None, dtype=None, stream=None) -> torch.Tensor:
+    """As cache_attention for a tree of drafted tokens: the new tokens of a sequence are nodes, which see every
+    key before the new ones and the nodes m whose bit m % 64 of word m // 64 of their row of tree [T, words]
+    (int64) is set -- their ancestors and themselves. positions [T] int32: the nodes' (as given to cache_append)."""
+    if tree is None or positions is None:
+        raise QPGError(QPG_EINVAL, "tree and positions must be given")
+    return _attention(q, k_cache, v_cache, table, lens, offsets, scale, cap, slopes, window, None, tree, positions, y, ws, dtype,
+                      stream, "cache_attention_tree")

@@ -1,0 +1,661 @@
+// Attention of new tokens over a paged cache of keys and values (include/qpg.h, cache_attention and
+// cache_attention_tree).
+//
+//   y = sum over seen keys of exp(s_j - m) v_j / sum of exp(s_j - m),  s = cap(scale <q, k>) - slope |i - j|
+//
+// One pass over the keys with the running maximum m and sum. The query rows of one key head -- its
+// new tokens times its G query heads, token by token -- are the columns of the matrix products, so prompts,
+// single tokens and trees are one kernel, and a key is read once for all that share it. A tile is BC = 32 * WC columns
+// of one sequence and key head. Products are taken transposed, with 32 x 32 x 16 matrix instructions:
+//   S^T [keys][columns] = K Q^T,   O^T [dim][columns] = V^T P^T.
+// A column is then a lane (and its partner 32 away) in both results: the softmax needs one exchange a stage,
+// the scaling of O no exchange, and P^T goes from the first result to the second operand in its own lane, since the
+// order of the keys in a product is free: register r of a lane in half h is key 8 (r >> 2) + 4h + (r & 3), and V^T
+// is read as the same keys, four at a time, by the transposing LDS read.
+//
+// Keys and values go from memory straight to LDS, a stage ahead; 16-byte slot c of row r holds
+// piece c ^ swizzle(r), which spreads both kinds of reads over all banks, and is made by the loads'
+// source offsets. Rows behind the sequence's end and pieces behind dim come from behind the descriptor's
+// end: zeros. A 16-row block lies in one page, and has its own descriptor: 64-bit page addresses.
+#include "qpg_cache.h"
+
+namespace qpg {
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) shortx4 lds_shortx4;
+typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
+
+struct AttentionArgs {
+    CacheBatch batch;
+    const void *q, *k, *v;
+    void* y;
+    float* part_o;                // [splits][T * heads][dim]
+    floatx2* part_ml;             // [splits][T * heads]: maximum (of scores in powers of two), sum
+    int64_t k_page, v_page;       // elements from page to page
+    int pages, page_bits, dim, heads, kv, group, slots, splits, y_type;
+    float scale, cap;             // scale * log2(e); cap * log2(e) with cap_scale = 2 scale / cap * log2(e)
+    float cap_scale;
+    const float* slopes;
+    int window;                   // 2^30 and more: none
+    const int32_t* prefix;
+    const int64_t* tree;
+    const int32_t* positions;
+    int words;
+};
+
+template <typename T> struct Matrix;
+template <> struct Matrix<_Float16> {
+    typedef halfx8 x8;
+    static constexpr unsigned INF = 0x7C00;
+    static constexpr unsigned ONE = 0x3C00;
+    static constexpr int LIFT = 6;            // shares are 2^6 times their value: small ones stay normal numbers
+    static constexpr int PIECES = 2;
+    static __device__ __forceinline__ floatx16 mul(x8 a, x8 b, floatx16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+template <> struct Matrix<__bf16> {
+    typedef bf16x8 x8;
+    static constexpr unsigned INF = 0x7F80;
+    static constexpr unsigned ONE = 0x3F80;
+    static constexpr int LIFT = 0;
+    static constexpr int PIECES = 3;
+    static __device__ __forceinline__ floatx16 mul(x8 a, x8 b, floatx16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+// Each lane's 16 bytes at voff go to LDS byte lds_wave_base + 16 * lane. Inline asm, so that the
+// compiler's own waits leave the prefetch alone; the kernel waits before a stage is read. m0
+// carries the wave-uniform LDS address. The compiler does not look into the asm: five wait states, since
+// its scalar operands may come straight from a lane (v_readlane, v_readfirstlane).
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, unsigned lds_wave_base, unsigned voff)
+{
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(r), "{m0}"(lds_wave_base) : "memory");
+}
+
+// A descriptor of `bytes` bytes from p, both the same for the wave.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int bytes)
+{
+    const uint64_t a = (uint64_t)p;
+    const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)a), hi = __builtin_amdgcn_readfirstlane((unsigned)(a >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
+constexpr unsigned NOWHERE = 0xFFFFFFF0u;      // past the end of every descriptor here
+
+// Both halves' maximum, in both.
+__device__ __forceinline__ float half_max(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The slot of a row's 16-byte piece: piece ^ swizzle(row). Rows of 64 values (two to a bank cycle of
+// 256 bytes), or of 128 and 256.
+template <int DP>
+__device__ __forceinline__ int swizzle(int row)
+{
+    return DP == 64 ? (((row >> 1) & 1) << 2) | ((row >> 2) & 3) : ((row & 3) << 2) | ((row >> 2) & 3);
+}
+
+template <int DP, int KT, int WK>
+struct AttentionLds {
+    static constexpr int STAGE = KT * DP * 2;          // bytes of a stage's keys, or values
+    uint8_t k[WK][2][STAGE];
+    uint8_t v[WK][2][STAGE];
+};
+
+constexpr float FAR = -3.402823466e38f;        // in place of a maximum of nothing: finite, so differences are numbers
+
+// T: cache type; DP: dim rounded up to 64, 128, 256; WC waves of 32 columns each share a stage of KT
+// keys, WK such groups take every WK-th stage of the tile's keys and are joined at the end; NP: pieces of a share.
+template <typename T, int DP, int WC, int WK, int KT, int NP>
+__global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cache_attention_kernel(AttentionArgs a)
+{
+    typedef typename Matrix<T>::x8 x8;
+    constexpr int BC = 32 * WC, NS = KT / 32, ND = DP / 32, NK = DP / 16, NB = KT / WC < 16 ? 1 : KT / WC / 16;
+    constexpr int ROWS = KT / WC;                      // rows of a stage that a wave loads
+    constexpr int RPI = 512 / DP, LOADS = ROWS / RPI;  // rows of one load, loads of a wave
+    constexpr int STAGE = AttentionLds<DP, KT, WK>::STAGE;
+    constexpr size_t JOIN = WK > 1 ? (size_t)WC * WK * 32 * (DP * 4 + 8) : 0;      // groups joined: o, maxima and sums
+    __shared__ __align__(1024) uint8_t lds_raw[sizeof(AttentionLds<DP, KT, WK>) > JOIN ? sizeof(AttentionLds<DP, KT, WK>) : JOIN];
+    AttentionLds<DP, KT, WK>& lds = *reinterpret_cast<AttentionLds<DP, KT, WK>*>(lds_raw);
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l31 = lane & 31, half = lane >> 5, wc = wave % WC, wk = wave / WC;
+
+    // Head, slot, split of this workgroup: where the heads are a multiple of the eight dies, a
+    // head's tiles run on one of them and share its cache; tiles with the most keys first.
+    int unit = blockIdx.x, h;
+    const int per_head = a.slots * a.splits;
+    if (a.kv % 8 == 0) {
+        h = (unit & 7) + 8 * ((unit >> 3) / per_head);
+        unit = (unit >> 3) % per_head;
+    } else {
+        h = unit % a.kv;
+        unit = unit / a.kv;
+    }
+    const int split = unit % a.splits, slot = a.slots - 1 - unit / a.splits;
+
+    // Sequence b has slots first(b) .. first(b + 1): enough for its tiles wherever its rows begin.
+    auto first = [&](int i) { return (int64_t)a.batch.offset(i) * a.group / BC + i; };
+    const int b = last_not_above(a.batch.B, slot, first);
+    const int row0 = __builtin_amdgcn_readfirstlane(a.batch.offset(b));
+    const int news = __builtin_amdgcn_readfirstlane(a.batch.offset(b + 1)) - row0;
+    const int64_t tile0 = ((int64_t)slot - first(b)) * BC;
+    if (tile0 < 0 || tile0 >= (int64_t)news * a.group) return;      // the same for the whole workgroup
+    const int c0 = (int)tile0, columns = min(BC, news * a.group - c0);
+    const int n = min(max(__builtin_amdgcn_readfirstlane(a.batch.lens[b]), 0), a.batch.width << a.page_bits);
+    const int ctx = n - news;                          // below 0: the first rows have no place
+    const int prefix = a.prefix ? min(max(__builtin_amdgcn_readfirstlane(a.prefix[b]), 0), n) : 0;
+
+    // This lane's column. Columns behind the last do as the last does, and are not written.
+    const int col = 32 * wc + l31, own = c0 + min(col, columns - 1);
+    const int token = own / a.group, head = h * a.group + own % a.group;
+    auto position_of = [&](int t) {
+        return a.tree ? min(max(a.positions[row0 + t], 0), 1 << 30) : ctx + t;
+    };
+    const int position = position_of(token);
+    // The range of the positions of the tile's columns, and of this wave's.
+    int low, high, wave_low, wave_high;
+    if (a.tree) {
+        low = 1 << 30, high = 0;
+        if (a.window < 1 << 30)
+            for (int t = c0 / a.group + lane; t <= (c0 + columns - 1) / a.group; t += 64) {
+                low = min(low, position_of(t));
+                high = max(high, position_of(t));
+            }
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            low = min(low, __shfl_xor(low, m));
+            high = max(high, __shfl_xor(high, m));
+        }
+        low = wave_low = __builtin_amdgcn_readfirstlane(low);
+        high = wave_high = __builtin_amdgcn_readfirstlane(high);
+    } else {
+        low = ctx + c0 / a.group;
+        high = ctx + (c0 + columns - 1) / a.group;
+        wave_low = ctx + (c0 + min(32 * wc, columns - 1)) / a.group;
+        wave_high = ctx + (c0 + min(32 * wc + 31, columns - 1)) / a.group;
+    }
+    // Positions are at most 2^30 and windows are clamped to it: no difference here overflows.
+    const int begin = a.window < 1 << 30 ? max(low - a.window + 1, 0) : 0;
+    const int end = a.tree ? n : min(n, max(high + 1, prefix));
+    // Stages: those of the prefix, then those from the window on.
+    const int head_stages = (min(prefix, end) + KT - 1) / KT;
+    const int begin_stage = max(begin / KT, head_stages), end_stage = (end + KT - 1) / KT;
+    const int stages = head_stages + max(end_stage - begin_stage, 0);
+    auto key_of = [&](int i) { return (i < head_stages ? i : i - head_stages + begin_stage) * KT; };
+    const int share = ((stages + a.splits - 1) / a.splits + WK - 1) / WK * WK;
+    const int i0 = min(split * share, stages), i1 = min(i0 + share, stages);
+    const int rounds = (i1 - i0 + WK - 1) / WK;
+
+    // Columns of Q^T: 8 values of 16-byte piece 2t + half.
+    x8 qt[NK];
+    {
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)(row0 + token) * a.heads + head) * a.dim;
+#pragma unroll
+        for (int t = 0; t < NK; ++t) {
+            const int d = 8 * (2 * t + half);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) qt[t][i] = (T)0.0f;
+            if (d < a.dim) qt[t] = *reinterpret_cast<const x8*>(q + d);
+        }
+    }
+
+    // Loads of a stage: block j of 16 rows of this wave, by its page.
+    const T* kc = static_cast<const T*>(a.k) + ((int64_t)h << a.page_bits) * a.dim;
+    const T* vc = static_cast<const T*>(a.v) + ((int64_t)h << a.page_bits) * a.dim;
+    const int32_t* table = a.batch.table + (int64_t)b * a.batch.width;
+    const int in_wave = lane / (DP / 8), slot16 = lane % (DP / 8), row_bytes = a.dim * 2;
+    int pages[NB];
+    auto look_up = [&](int i) {
+        const int key = i < i1 ? key_of(i) : 0;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int at = (key + wc * ROWS + 16 * j) >> a.page_bits;
+            pages[j] = min(max(table[min(at, a.batch.width - 1)], 0), a.pages - 1);
+        }
+    };
+    const unsigned lds_k = (unsigned)(uintptr_t)(lds_void*)&lds.k[wk][0][0], lds_v = (unsigned)(uintptr_t)(lds_void*)&lds.v[wk][0][0];
+    auto load_stage = [&](int i, int buffer) {
+        const int key = i < i1 ? key_of(i) : 1 << 30;
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+            const int row = wc * ROWS + j * RPI, block = row & ~15;          // row of the stage
+            const int first_key = key + block, in_page = first_key & ((1 << a.page_bits) - 1);
+            const int there = min(max(n - first_key, 0), 16) * row_bytes;
+            const int r = row + in_wave, piece = slot16 ^ swizzle<DP>(r);
+            const unsigned voff = 8 * piece < a.dim ? (unsigned)((r - block) * row_bytes + 16 * piece) : NOWHERE;
+            const int page = pages[NB == 1 ? 0 : (j * RPI) / 16];
+            const int64_t in_block = (int64_t)in_page * a.dim;
+            load_to_lds(buffer_of(kc + page * a.k_page + in_block, there), lds_k + buffer * STAGE + row * DP * 2, voff);
+            load_to_lds(buffer_of(vc + page * a.v_page + in_block, there), lds_v + buffer * STAGE + row * DP * 2, voff);
+        }
+    };
+
+    floatx16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+    float m = FAR, sum = 0.0f;                         // m: in powers of two
+
+    // LDS places of this lane's operands in a stage.
+    const int k_place = l31 * DP * 2 + ((half ^ swizzle<DP>(l31)) << 4);       // piece 2t + half: ^ (t << 5)
+    const int i16 = lane & 15, v_row = 4 * half + (i16 >> 2);
+    int v_place[2];                                    // rows v_row and v_row + 8; columns of d tile 0: ^ (tile << 6)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int piece = ((lane >> 4) & 1) * 2 + ((i16 & 3) >> 1);
+        v_place[e] = (v_row + 8 * e) * DP * 2 + ((piece ^ swizzle<DP>(v_row + 8 * e)) << 4) + (i16 & 1) * 8;
+    }
+
+    if (rounds > 0) {
+        look_up(i0 + wk);
+        load_stage(i0 + wk, 0);
+        look_up(i0 + wk + WK);
+    }
+    for (int round = 0; round < rounds; ++round) {
+        const int i = i0 + wk + round * WK, buffer = round & 1;
+        // this stage has landed, and every wave is done with the other buffer
+        if (WC > 1)
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        if (round + 1 < rounds) {
+            load_stage(i + WK, buffer ^ 1);
+            look_up(i + 2 * WK);
+        }
+        if (i >= i1) continue;
+        const int key = key_of(i), last = key + KT - 1;
+        // a stage that none of the wave's columns sees
+        if (!a.tree && key >= prefix && (key > wave_high || last < wave_low - a.window + 1)) continue;
+
+        const uint8_t* kb = lds.k[wk][buffer];
+        const uint8_t* vb = lds.v[wk][buffer];
+        floatx16 s[NS];
+#pragma unroll
+        for (int e = 0; e < NS; ++e)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[e][r] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < NK; ++t)
+#pragma unroll
+            for (int e = 0; e < NS; ++e)
+                s[e] = Matrix<T>::mul(*reinterpret_cast<const x8*>(kb + e * 32 * DP * 2 + (k_place ^ (t << 5))), qt[t], s[e]);
+
+        // Scores in powers of two: c * s once cap and bias are in.
+        float c = a.scale;
+        if (a.cap > 0.0f) {
+            // cap tanh(x) = cap - 2 cap / (exp(2x) + 1); next to 0, where that cancels, by its series to x^9
+            // (the next term is below 2^-24 of x up to |x| = 0.2)
+            c = 1.0f;
+#pragma unroll
+            for (int e = 0; e < NS; ++e)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float x = s[e][r];
+                    const float big = a.cap - 2.0f * a.cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * a.cap_scale) + 1.0f);
+                    if (NP == 1) {
+                        s[e][r] = big;
+                    } else {
+                        const float z = x * (a.cap_scale * 0.34657359027997264f), z2 = z * z;    // ln(2) / 2
+                        const float small = a.cap * (z + z * z2 * (-0.33333333333f + z2 * (0.13333333333f +
+                                            z2 * (-0.053968253968f + z2 * 0.021869488536f))));
+                        s[e][r] = fabsf(z) < 0.2f ? small : big;
+                    }
+                }
+        }
+        const bool whole = a.tree ? last < ctx && (a.window >= 1 << 30 || high - key < a.window)
+                                  : last < n && (last < prefix || (last <= wave_low && wave_high - key < a.window));
+        if (a.slopes || !whole) {
+            const int limit = min(position, n - 1), from = a.window < 1 << 30 ? position - a.window + 1 : -1;
+            const float slope = a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.0f;
+            const int64_t* bits = a.tree ? a.tree + (int64_t)(row0 + token) * a.words : nullptr;
+#pragma unroll
+            for (int e = 0; e < NS; ++e)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int j = key + 32 * e + 8 * (r >> 2) + 4 * half + (r & 3);
+                    int at = j;
+                    bool seen;
+                    if (a.tree && j >= ctx) {
+                        const int node = j - ctx;
+                        const bool there = j < n && node < news;
+                        const int word = min(node >> 6, a.words - 1);
+                        seen = there && node < 64 * a.words && ((bits[word] >> (node & 63)) & 1);
+                        if (there) at = min(max(a.positions[row0 + node], 0), 1 << 30);
+                        seen = seen && at >= from;
+                    } else {
+                        seen = (j >= from && j <= (a.tree ? n - 1 : limit)) || j < prefix;
+                    }
+                    float x = s[e][r] * c;
+                    if (a.slopes) x -= slope * (float)(position > at ? position - at : at - position);
+                    s[e][r] = seen ? x : -INFINITY;
+                }
+            c = 1.0f;
+        }
+
+        // Running maximum. It is moved only when it has grown by 2^8 (8 bits of f32's, and f16's, range are spare).
+        float top = s[0][0];
+#pragma unroll
+        for (int e = 0; e < NS; ++e)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[e][r]);
+        top = half_max(top) * c;
+        if (__ballot(top > m + 8.0f)) {
+            const float next = fmaxf(m, top), shrink = __builtin_amdgcn_exp2f(m - next);
+            m = next;
+            sum *= shrink;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[d][r] *= shrink;
+        }
+        const float base = (float)Matrix<T>::LIFT - m;
+        float part = 0.0f;
+        x8 p[NP][2 * NS];
+#pragma unroll
+        for (int e = 0; e < NS; ++e)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e][r], c, base));
+                part += x;
+                float rest = x;
+#pragma unroll
+                for (int f = 0; f < NP; ++f) {
+                    const T piece = (T)rest;           // to nearest even; the next piece is what it left
+                    p[f][2 * e + (r >> 3)][r & 7] = piece;
+                    rest -= (float)piece;
+                }
+            }
+        sum += part;
+
+        // V^T rows 32d .. 32d + 31, keys 16f + 4 half + 0..3 and + 8
+        auto values = [&](int f, int d) {
+            union { shortx4 s[2]; x8 v; } u;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)(vb + f * 16 * DP * 2 + (v_place[e] ^ (d << 6))));
+            return u.v;
+        };
+        // A value that is no number times a share of 0 would be NaN. Rows that one column of the wave sees
+        // and another does not are looked through for such values.
+        bool odd = false;
+        if (!whole) {
+            const int upto = min(last, n - 1);
+            const bool mixed = a.tree ? upto >= ctx || high - key >= a.window
+                                      : !(upto < prefix || (upto <= wave_low && wave_high - key < a.window));
+            if (mixed) {
+                ushortx2 most = {0, 0};
+                for (int at = lane * 16; at < STAGE; at += 1024) {
+                    const uint32x4 x = *reinterpret_cast<const uint32x4*>(vb + at);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const unsigned w = x[e] & 0x7FFF7FFFu;
+                        most = __builtin_elementwise_max(most, __builtin_bit_cast(ushortx2, w));
+                    }
+                }
+                odd = __ballot(max(most[0], most[1]) >= Matrix<T>::INF) != 0;
+            }
+        }
+        if (!odd) {
+#pragma unroll
+            for (int f = 0; f < 2 * NS; ++f)
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    const x8 v = values(f, d);
+#pragma unroll
+                    for (int g = 0; g < NP; ++g) o[d] = Matrix<T>::mul(v, p[g][f], o[d]);
+                }
+        } else {
+            // Finite values as ever. Of the others, how many with a share there are: of +infinity or NaN, and of
+            // -infinity or NaN. Both: NaN.
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                floatx16 up, down;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) up[r] = down[r] = 0.0f;
+#pragma unroll
+                for (int f = 0; f < 2 * NS; ++f) {
+                    union { x8 v; unsigned short u[8]; } v, vu, vd, on;
+                    v.v = values(f, d);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const unsigned bits = v.u[e], size = bits & 0x7FFF;
+                        const bool nan = size > Matrix<T>::INF, inf = size == Matrix<T>::INF;
+                        vu.u[e] = nan || (inf && !(bits >> 15)) ? Matrix<T>::ONE : 0;
+                        vd.u[e] = nan || (inf && (bits >> 15)) ? Matrix<T>::ONE : 0;
+                        v.u[e] = nan || inf ? 0 : bits;
+                        on.u[e] = (float)p[0][f][e] != 0.0f ? Matrix<T>::ONE : 0;
+                    }
+#pragma unroll
+                    for (int g = 0; g < NP; ++g) o[d] = Matrix<T>::mul(v.v, p[g][f], o[d]);
+                    up = Matrix<T>::mul(vu.v, on.v, up);
+                    down = Matrix<T>::mul(vd.v, on.v, down);
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    if (up[r] > 0.0f) o[d][r] += INFINITY;
+                    if (down[r] > 0.0f) o[d][r] -= INFINITY;
+                }
+            }
+        }
+    }
+    m -= (float)Matrix<T>::LIFT;                       // sum and o are of powers relative to this
+    sum = half_sum(sum);
+
+    // Groups of one column joined: all to the largest maximum, then added in their order.
+    if constexpr (WK > 1) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        constexpr int WAVES = WC * WK;
+        float* join = reinterpret_cast<float*>(lds_raw);          // [waves][ND][4][64] x 4, then maxima and sums
+        floatx2* ml = reinterpret_cast<floatx2*>(lds_raw + (size_t)WAVES * DP * 32 * 4);
+        if (half == 0) ml[wave * 32 + l31] = floatx2{m, sum};
+        __syncthreads();
+        float top = m;
+#pragma unroll
+        for (int g = 0; g < WK; ++g) top = fmaxf(top, ml[(g * WC + wc) * 32 + l31][0]);
+        const float shrink = __builtin_amdgcn_exp2f(m - top);
+        sum = 0.0f;
+#pragma unroll
+        for (int g = 0; g < WK; ++g) {
+            const floatx2 x = ml[(g * WC + wc) * 32 + l31];
+            sum += x[1] * __builtin_amdgcn_exp2f(x[0] - top);
+        }
+        m = top;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                floatx4 x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = o[d][4 * r + e] * shrink;
+                *reinterpret_cast<floatx4*>(join + (((size_t)wave * ND + d) * 4 + r) * 256 + lane * 4) = x;
+            }
+        __syncthreads();
+        // wave wk of the columns adds up the quarters d * 4 + r with that number
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if ((d * 4 + r) % WK != wk) continue;
+                floatx4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int g = 0; g < WK; ++g) {
+                    const floatx4 z = *reinterpret_cast<const floatx4*>(join + (((size_t)(g * WC + wc) * ND + d) * 4 + r) * 256 + lane * 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] += z[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[d][4 * r + e] = x[e];
+            }
+    }
+
+    if (col >= columns) return;
+    const int64_t row = (int64_t)(row0 + token) * a.heads + head;
+    const bool parts = a.splits > 1;
+    const int64_t part_row = (int64_t)split * a.batch.T * a.heads + row;
+    if (parts && half == 0 && wk == 0) a.part_ml[part_row] = floatx2{m, sum};
+    if (parts && rounds == 0) return;
+    const float inv = parts ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (WK > 1 && (d * 4 + r) % WK != wk) continue;
+            const int at = 32 * d + 8 * r + 4 * half;
+            if (at >= a.dim) continue;
+            floatx4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = o[d][4 * r + e] * inv;
+            if (parts) {
+                *reinterpret_cast<floatx4*>(a.part_o + part_row * a.dim + at) = x;
+            } else if (a.y_type == QPG_F32) {
+                *reinterpret_cast<floatx4*>(static_cast<float*>(a.y) + row * a.dim + at) = x;
+            } else if (a.y_type == QPG_F16) {
+                *reinterpret_cast<Pack<_Float16, 4>*>(static_cast<_Float16*>(a.y) + row * a.dim + at) =
+                    Pack<_Float16, 4>{(_Float16)x[0], (_Float16)x[1], (_Float16)x[2], (_Float16)x[3]};
+            } else {
+                *reinterpret_cast<Pack<__bf16, 4>*>(static_cast<__bf16*>(a.y) + row * a.dim + at) =
+                    Pack<__bf16, 4>{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+            }
+        }
+}
+
+// The pieces of a row's keys: y = sum of 2^(m_s - m) o_s / sum of 2^(m_s - m) sum_s, s upwards. A thread has four values.
+template <typename TY>
+__global__ void __launch_bounds__(256) cache_attention_join_kernel(const float* __restrict__ part_o,
+                                                                   const floatx2* __restrict__ part_ml, TY* __restrict__ y,
+                                                                   CacheBatch batch, int64_t rows, int heads, int dim,
+                                                                   int splits)
+{
+    const int fours = dim / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / fours;
+    if (row >= rows) return;
+    const int t = (int)(row / heads), at = (int)(i % fours) * 4;
+    if (t < batch.offset(0) || t >= batch.offset(batch.B)) return;
+    float m = FAR;
+    for (int s = 0; s < splits; ++s) {
+        const floatx2 x = part_ml[s * rows + row];
+        if (x[1] != 0.0f) m = fmaxf(m, x[0]);
+    }
+    float sum = 0.0f;
+    floatx4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < splits; ++s) {
+        const floatx2 x = part_ml[s * rows + row];
+        if (x[1] == 0.0f) continue;
+        const float w = __builtin_amdgcn_exp2f(x[0] - m);
+        const floatx4 z = *reinterpret_cast<const floatx4*>(part_o + (s * rows + row) * dim + at);
+        sum += w * x[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += w * z[e];
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    Pack<TY, 4> x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x.v[e] = (TY)(o[e] * inv);
+    *reinterpret_cast<Pack<TY, 4>*>(y + row * dim + at) = x;
+}
+
+}  // namespace qpg
+
+namespace {
+
+// Columns of a tile, by the columns that a sequence has on average.
+int tile_columns(int64_t T, int64_t B, int64_t group)
+{
+    const int64_t mean = (T * group + B - 1) / B;
+    return mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+}
+
+}  // namespace
+
+int qpg_cache_attention_splits(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length)
+{
+    const int64_t group = heads / kv, bc = tile_columns(T, B, group);
+    const int64_t tiles = ((T * group + bc - 1) / bc > (B < T ? B : T) ? (T * group + bc - 1) / bc : (B < T ? B : T)) * kv;
+    // pieces of at least 256 keys, and about 1024 workgroups
+    int64_t splits = 1024 / tiles;
+    if (splits > length / 256) splits = length / 256;
+    if (splits > 64) splits = 64;
+    return splits < 1 ? 1 : (int)splits;
+}
+
+int64_t qpg_cache_attention_grid(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length)
+{
+    const int64_t group = heads / kv;
+    return (T * group / tile_columns(T, B, group) + B) * kv * qpg_cache_attention_splits(T, B, heads, kv, dim, length);
+}
+
+hipError_t qpg_launch_cache_attention(const qpg_cache& cache, const qpg_batch& batch, const qpg_scores& scores,
+                                      const void* q, int64_t heads, const int64_t* tree, int64_t words,
+                                      const int32_t* positions, void* y, int y_type, void* ws, hipStream_t s)
+{
+    using namespace qpg;
+    const int64_t group = heads / cache.heads, bc = tile_columns(batch.T, batch.B, group);
+    int page_bits = 0;
+    while ((1 << page_bits) < cache.page) ++page_bits;
+    const int64_t length = batch.width * cache.page, rows = batch.T * heads, slots = batch.T * group / bc + batch.B;
+    const int splits = qpg_cache_attention_splits(batch.T, batch.B, heads, cache.heads, cache.dim, length);
+    constexpr float LOG2E = 1.4426950408889634f;
+    const bool capped = scores.cap > 0.0f;
+    AttentionArgs a = {{batch.table, batch.lens, batch.offsets, (int)batch.B, (int)batch.width, (int)batch.T},
+                       q, cache.k, cache.v, y, static_cast<float*>(ws),
+                       reinterpret_cast<floatx2*>(static_cast<float*>(ws) + (splits > 1 ? splits * rows * cache.dim : 0)),
+                       cache.k_stride, cache.v_stride, (int)cache.pages, page_bits, (int)cache.dim, (int)heads,
+                       (int)cache.heads, (int)group, (int)slots, splits, y_type,
+                       scores.scale * LOG2E, capped ? scores.cap * LOG2E : 0.0f,
+                       capped ? 2.0f * scores.scale / scores.cap * LOG2E : 0.0f, scores.slopes,
+                       scores.window > 0 && scores.window < 1 << 30 ? (int)scores.window : 1 << 30, scores.prefix, tree,
+                       positions, (int)words};
+    const bool fine = y_type == QPG_F32 || (y_type == QPG_F16 && cache.type == QPG_BF16);
+    const dim3 grid((unsigned)(slots * cache.heads * splits));
+    auto launch = [&](auto t, auto dp, auto wc, auto wk, auto kt) {
+        typedef typename Store<decltype(t)::value>::type T;
+        constexpr int DP = decltype(dp)::value, WC = decltype(wc)::value, WK = decltype(wk)::value, KT = decltype(kt)::value;
+        if (fine)
+            hipLaunchKernelGGL((cache_attention_kernel<T, DP, WC, WK, KT, Matrix<T>::PIECES>), grid, dim3(64 * WC * WK), 0, s, a);
+        else
+            hipLaunchKernelGGL((cache_attention_kernel<T, DP, WC, WK, KT, 1>), grid, dim3(64 * WC * WK), 0, s, a);
+        return hipGetLastError();
+    };
+    using std::integral_constant;
+    auto by_columns = [&](auto t, auto dp) {
+        constexpr int DP = decltype(dp)::value, KT = DP == 256 ? 32 : 64;
+        if (bc == 128) return launch(t, dp, integral_constant<int, 4>(), integral_constant<int, 1>(), integral_constant<int, KT>());
+        if constexpr (DP == 256) {
+            if (bc == 64) return launch(t, dp, integral_constant<int, 2>(), integral_constant<int, 2>(), integral_constant<int, 32>());
+            return launch(t, dp, integral_constant<int, 1>(), integral_constant<int, 2>(), integral_constant<int, 32>());
+        } else {
+            if (bc == 64) return launch(t, dp, integral_constant<int, 2>(), integral_constant<int, 2>(), integral_constant<int, 32>());
+            return launch(t, dp, integral_constant<int, 1>(), integral_constant<int, 4>(), integral_constant<int, 32>());
+        }
+    };
+    auto by_dim = [&](auto t) {
+        if (cache.dim <= 64) return by_columns(t, integral_constant<int, 64>());
+        if (cache.dim <= 128) return by_columns(t, integral_constant<int, 128>());
+        return by_columns(t, integral_constant<int, 256>());
+    };
+    const hipError_t e = cache.type == QPG_F16 ? by_dim(integral_constant<int, QPG_F16>())
+                                               : by_dim(integral_constant<int, QPG_BF16>());
+    if (e != hipSuccess || splits == 1) return e;
+    return qpg_by_type(y_type, [&](auto t) {
+        typedef typename Store<decltype(t)::value>::type TY;
+        const int64_t threads = rows * (cache.dim / 4);
+        hipLaunchKernelGGL(cache_attention_join_kernel<TY>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s,
+                           a.part_o, a.part_ml, static_cast<TY*>(y), a.batch, rows, (int)heads, (int)cache.dim, splits);
+        return hipGetLastError();
+    });
+}
