@@ -37,7 +37,7 @@ struct AttentionArgs {
     float scale, cap;             // scale * log2(e); cap * log2(e) with cap_scale = 2 scale / cap * log2(e)
     float cap_scale;
     const float* slopes;
-    int window;                   // 2^30 and more: none
+    int window;                   // NO_WINDOW and more: none
     const int32_t* prefix;
     const int64_t* tree;
     const int32_t* positions;
@@ -48,7 +48,6 @@ template <typename T> struct Matrix;
 template <> struct Matrix<_Float16> {
     typedef halfx8 x8;
     static constexpr unsigned INF = 0x7C00;
-    static constexpr unsigned ONE = 0x3C00;
     static constexpr int LIFT = 6;            // shares are 2^6 times their value: small ones stay normal numbers
     static constexpr int PIECES = 2;
     static __device__ __forceinline__ floatx16 mul(x8 a, x8 b, floatx16 c)
@@ -59,7 +58,6 @@ template <> struct Matrix<_Float16> {
 template <> struct Matrix<__bf16> {
     typedef bf16x8 x8;
     static constexpr unsigned INF = 0x7F80;
-    static constexpr unsigned ONE = 0x3F80;
     static constexpr int LIFT = 0;
     static constexpr int PIECES = 3;
     static __device__ __forceinline__ floatx16 mul(x8 a, x8 b, floatx16 c)
@@ -98,6 +96,23 @@ __device__ __forceinline__ float half_sum(float x)
 {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+constexpr int NO_WINDOW = 1 << 30;
+constexpr float LOG2E = 1.4426950408889634f;
+
+// cap tanh(x) = cap - 2 cap / (exp(2x) + 1), with `cap` in powers of two and exp(2x) = 2^(s * cap_scale). Next to 0, where
+// that cancels, FINE takes the series to x^9 (the next term is below 2^-24 of x up to |x| = 0.2); without it the
+// error is a few steps of 1 times the cap, far below a share's rounding to 16 bits.
+template <bool FINE>
+__device__ __forceinline__ float capped(float s, float cap, float cap_scale)
+{
+    const float t = s * cap_scale;
+    const float big = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(t) + 1.0f);
+    if (!FINE) return big;
+    const float z = t * 0.34657359027997264f, z2 = z * z;               // ln(2) / 2
+    const float small = cap * (z + z * z2 * (-0.33333333333f + z2 * (0.13333333333f + z2 * (-0.053968253968f + z2 * 0.021869488536f))));
+    return fabsf(z) < 0.2f ? small : big;
 }
 
 // The slot of a row's 16-byte piece: piece ^ swizzle(row). Rows of 64 values (two to a bank cycle of
@@ -170,7 +185,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     int low, high, wave_low, wave_high;
     if (a.tree) {
         low = 1 << 30, high = 0;
-        if (a.window < 1 << 30)
+        if (a.window < NO_WINDOW)
             for (int t = c0 / a.group + lane; t <= (c0 + columns - 1) / a.group; t += 64) {
                 low = min(low, position_of(t));
                 high = max(high, position_of(t));
@@ -189,7 +204,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         wave_high = ctx + (c0 + min(32 * wc + 31, columns - 1)) / a.group;
     }
     // Positions are at most 2^30 and windows are clamped to it: no difference here overflows.
-    const int begin = a.window < 1 << 30 ? max(low - a.window + 1, 0) : 0;
+    const int begin = a.window < NO_WINDOW ? max(low - a.window + 1, 0) : 0;
     const int end = a.tree ? n : min(n, max(high + 1, prefix));
     // Stages: those of the prefix, then those from the window on.
     const int head_stages = (min(prefix, end) + KT - 1) / KT;
@@ -217,7 +232,13 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     const T* kc = static_cast<const T*>(a.k) + ((int64_t)h << a.page_bits) * a.dim;
     const T* vc = static_cast<const T*>(a.v) + ((int64_t)h << a.page_bits) * a.dim;
     const int32_t* table = a.batch.table + (int64_t)b * a.batch.width;
-    const int in_wave = lane / (DP / 8), slot16 = lane % (DP / 8), row_bytes = a.dim * 2;
+    const int row_bytes = a.dim * 2;
+    unsigned voff[LOADS];                              // from the first row of its block
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+        const int r = wc * ROWS + j * RPI + lane / (DP / 8), piece = (lane % (DP / 8)) ^ swizzle<DP>(r);
+        voff[j] = 8 * piece < a.dim ? (unsigned)((r & 15) * row_bytes + 16 * piece) : NOWHERE;
+    }
     int pages[NB];
     auto look_up = [&](int i) {
         const int key = i < i1 ? key_of(i) : 0;
@@ -235,12 +256,10 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
             const int row = wc * ROWS + j * RPI, block = row & ~15;          // row of the stage
             const int first_key = key + block, in_page = first_key & ((1 << a.page_bits) - 1);
             const int there = min(max(n - first_key, 0), 16) * row_bytes;
-            const int r = row + in_wave, piece = slot16 ^ swizzle<DP>(r);
-            const unsigned voff = 8 * piece < a.dim ? (unsigned)((r - block) * row_bytes + 16 * piece) : NOWHERE;
             const int page = pages[NB == 1 ? 0 : (j * RPI) / 16];
             const int64_t in_block = (int64_t)in_page * a.dim;
-            load_to_lds(buffer_of(kc + page * a.k_page + in_block, there), lds_k + buffer * STAGE + row * DP * 2, voff);
-            load_to_lds(buffer_of(vc + page * a.v_page + in_block, there), lds_v + buffer * STAGE + row * DP * 2, voff);
+            load_to_lds(buffer_of(kc + page * a.k_page + in_block, there), lds_k + buffer * STAGE + row * DP * 2, voff[j]);
+            load_to_lds(buffer_of(vc + page * a.v_page + in_block, there), lds_v + buffer * STAGE + row * DP * 2, voff[j]);
         }
     };
 
@@ -250,6 +269,31 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
     float m = FAR, sum = 0.0f;                         // m: in powers of two
+    bool odd = false;
+
+    // The first seen key position of this column, the position of a key, and the seen ones of keys j .. j + 63 as bits
+    // (of nodes without the window).
+    const int from = a.window < NO_WINDOW ? position - a.window + 1 : -1;
+    auto key_position = [&](int j) {
+        return a.tree && j >= ctx ? position_of(min(j - ctx, news - 1)) : j;
+    };
+    auto seen_from = [&](int j) {
+        auto range = [&](int lo, int hi) -> uint64_t {
+            const int x = max(lo - j, 0), z = min(hi - j, 63);
+            return z < x ? 0 : (~(uint64_t)0 << x) & (~(uint64_t)0 >> (63 - z));
+        };
+        if (!a.tree) return range(from, min(position, n - 1)) | range(0, prefix - 1);
+        uint64_t seen = range(from, min(ctx, n) - 1);
+        if (j + 63 >= ctx) {
+            const int64_t* row = a.tree + (int64_t)(row0 + token) * a.words;
+            auto word = [&](int i) { return i >= 0 && i < a.words ? (uint64_t)row[i] : 0; };
+            const int node = j - ctx, shift = node & 63;
+            uint64_t bits = word(node >> 6) >> shift;
+            if (shift) bits |= word((node >> 6) + 1) << (64 - shift);
+            seen |= bits & range(max(ctx, 0), n - 1);
+        }
+        return seen;
+    };
 
     // LDS places of this lane's operands in a stage.
     const int k_place = l31 * DP * 2 + ((half ^ swizzle<DP>(l31)) << 4);       // piece 2t + half: ^ (t << 5)
@@ -298,53 +342,62 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         // Scores in powers of two: c * s once cap and bias are in.
         float c = a.scale;
         if (a.cap > 0.0f) {
-            // cap tanh(x) = cap - 2 cap / (exp(2x) + 1); next to 0, where that cancels, by its series to x^9
-            // (the next term is below 2^-24 of x up to |x| = 0.2)
             c = 1.0f;
 #pragma unroll
             for (int e = 0; e < NS; ++e)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float x = s[e][r];
-                    const float big = a.cap - 2.0f * a.cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * a.cap_scale) + 1.0f);
-                    if (NP == 1) {
-                        s[e][r] = big;
-                    } else {
-                        const float z = x * (a.cap_scale * 0.34657359027997264f), z2 = z * z;    // ln(2) / 2
-                        const float small = a.cap * (z + z * z2 * (-0.33333333333f + z2 * (0.13333333333f +
-                                            z2 * (-0.053968253968f + z2 * 0.021869488536f))));
-                        s[e][r] = fabsf(z) < 0.2f ? small : big;
-                    }
-                }
+                for (int r = 0; r < 16; ++r) s[e][r] = capped<(NP > 1)>(s[e][r], a.cap, a.cap_scale);
         }
-        const bool whole = a.tree ? last < ctx && (a.window >= 1 << 30 || high - key < a.window)
+        const bool whole = a.tree ? last < ctx && (a.window >= NO_WINDOW || high - key < a.window)
                                   : last < n && (last < prefix || (last <= wave_low && wave_high - key < a.window));
         if (a.slopes || !whole) {
-            const int limit = min(position, n - 1), from = a.window < 1 << 30 ? position - a.window + 1 : -1;
-            const float slope = a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.0f;
-            const int64_t* bits = a.tree ? a.tree + (int64_t)(row0 + token) * a.words : nullptr;
+            // Bit i of `seen`: key + i is seen. Node positions, where they matter, are fetched by the lanes together.
+            const bool placed = a.tree && last >= ctx && (a.slopes || a.window < NO_WINDOW);
+            const int at_lane = placed ? key_position(key + lane) : 0;
+            uint64_t seen = seen_from(key);
+            if (a.slopes) {
+                const float slope = -a.slopes[head] * LOG2E, gap = (float)(position - key - 4 * half);
 #pragma unroll
-            for (int e = 0; e < NS; ++e)
+                for (int e = 0; e < NS; ++e)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int i = 32 * e + 8 * (r >> 2) + (r & 3);
+                        const float far = placed ? (float)(position - __shfl(at_lane, i + 4 * half)) : gap - (float)i;
+                        s[e][r] = __builtin_fmaf(slope, fabsf(far), s[e][r] * c);
+                    }
+                c = 1.0f;
+            }
+            seen >>= 4 * half;
+#pragma unroll
+            for (int e = 0; e < NS; ++e) {
+                const uint32_t bits = (uint32_t)(seen >> (32 * e));
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int j = key + 32 * e + 8 * (r >> 2) + 4 * half + (r & 3);
-                    int at = j;
-                    bool seen;
-                    if (a.tree && j >= ctx) {
-                        const int node = j - ctx;
-                        const bool there = j < n && node < news;
-                        const int word = min(node >> 6, a.words - 1);
-                        seen = there && node < 64 * a.words && ((bits[word] >> (node & 63)) & 1);
-                        if (there) at = min(max(a.positions[row0 + node], 0), 1 << 30);
-                        seen = seen && at >= from;
-                    } else {
-                        seen = (j >= from && j <= (a.tree ? n - 1 : limit)) || j < prefix;
+                    const int i = 8 * (r >> 2) + (r & 3);
+                    bool on = (bits >> i) & 1;
+                    if (placed) {
+                        const int at = __shfl(at_lane, 32 * e + i + 4 * half);         // by all lanes
+                        on = on && at >= from;
                     }
-                    float x = s[e][r] * c;
-                    if (a.slopes) x -= slope * (float)(position > at ? position - at : at - position);
-                    s[e][r] = seen ? x : -INFINITY;
+                    s[e][r] = on ? s[e][r] : -INFINITY;
                 }
-            c = 1.0f;
+            }
+            // A value that is no number times a share of 0 would be NaN. Rows that one column of the wave sees and
+            // another does not are looked through for such values; where there are any, the columns are done again below.
+            const int upto = min(last, n - 1);
+            const bool mixed = a.tree ? upto >= ctx || high - key >= a.window
+                                      : !(upto < prefix || (upto <= wave_low && wave_high - key < a.window));
+            if (mixed) {
+                ushortx2 most = {0, 0};
+#pragma unroll 4
+                for (int at = lane * 16; at < STAGE; at += 1024) {
+                    const uint32x4 x = *reinterpret_cast<const uint32x4*>(vb + at);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        most = __builtin_elementwise_max(most, __builtin_bit_cast(ushortx2, x[e] & 0x7FFF7FFFu));
+                }
+                odd |= __ballot(max(most[0], most[1]) >= Matrix<T>::INF) != 0;
+            }
         }
 
         // Running maximum. It is moved only when it has grown by 2^8 (8 bits of f32's, and f16's, range are spare).
@@ -365,93 +418,80 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         }
         const float base = (float)Matrix<T>::LIFT - m;
         float part = 0.0f;
-        x8 p[NP][2 * NS];
 #pragma unroll
         for (int e = 0; e < NS; ++e)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e][r], c, base));
-                part += x;
-                float rest = x;
+                s[e][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e][r], c, base));
+                part += s[e][r];
+            }
+        sum += part;
+        // V^T rows 32d .. 32d + 31, keys 16f + 4 half + 0..3 and + 8
 #pragma unroll
-                for (int f = 0; f < NP; ++f) {
+        for (int f = 0; f < 2 * NS; ++f) {
+            x8 p[NP];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float rest = s[f >> 1][8 * (f & 1) + i];
+#pragma unroll
+                for (int g = 0; g < NP; ++g) {
                     const T piece = (T)rest;           // to nearest even; the next piece is what it left
-                    p[f][2 * e + (r >> 3)][r & 7] = piece;
+                    p[g][i] = piece;
                     rest -= (float)piece;
                 }
             }
-        sum += part;
-
-        // V^T rows 32d .. 32d + 31, keys 16f + 4 half + 0..3 and + 8
-        auto values = [&](int f, int d) {
-            union { shortx4 s[2]; x8 v; } u;
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)(vb + f * 16 * DP * 2 + (v_place[e] ^ (d << 6))));
-            return u.v;
-        };
-        // A value that is no number times a share of 0 would be NaN. Rows that one column of the wave sees
-        // and another does not are looked through for such values.
-        bool odd = false;
-        if (!whole) {
-            const int upto = min(last, n - 1);
-            const bool mixed = a.tree ? upto >= ctx || high - key >= a.window
-                                      : !(upto < prefix || (upto <= wave_low && wave_high - key < a.window));
-            if (mixed) {
-                ushortx2 most = {0, 0};
-                for (int at = lane * 16; at < STAGE; at += 1024) {
-                    const uint32x4 x = *reinterpret_cast<const uint32x4*>(vb + at);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const unsigned w = x[e] & 0x7FFF7FFFu;
-                        most = __builtin_elementwise_max(most, __builtin_bit_cast(ushortx2, w));
-                    }
-                }
-                odd = __ballot(max(most[0], most[1]) >= Matrix<T>::INF) != 0;
-            }
-        }
-        if (!odd) {
-#pragma unroll
-            for (int f = 0; f < 2 * NS; ++f)
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    const x8 v = values(f, d);
-#pragma unroll
-                    for (int g = 0; g < NP; ++g) o[d] = Matrix<T>::mul(v, p[g][f], o[d]);
-                }
-        } else {
-            // Finite values as ever. Of the others, how many with a share there are: of +infinity or NaN, and of
-            // -infinity or NaN. Both: NaN.
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                floatx16 up, down;
+                union { shortx4 s[2]; x8 v; } u;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) up[r] = down[r] = 0.0f;
+                for (int e = 0; e < 2; ++e)
+                    u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)(vb + f * 16 * DP * 2 + (v_place[e] ^ (d << 6))));
 #pragma unroll
-                for (int f = 0; f < 2 * NS; ++f) {
-                    union { x8 v; unsigned short u[8]; } v, vu, vd, on;
-                    v.v = values(f, d);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const unsigned bits = v.u[e], size = bits & 0x7FFF;
-                        const bool nan = size > Matrix<T>::INF, inf = size == Matrix<T>::INF;
-                        vu.u[e] = nan || (inf && !(bits >> 15)) ? Matrix<T>::ONE : 0;
-                        vd.u[e] = nan || (inf && (bits >> 15)) ? Matrix<T>::ONE : 0;
-                        v.u[e] = nan || inf ? 0 : bits;
-                        on.u[e] = (float)p[0][f][e] != 0.0f ? Matrix<T>::ONE : 0;
-                    }
-#pragma unroll
-                    for (int g = 0; g < NP; ++g) o[d] = Matrix<T>::mul(v.v, p[g][f], o[d]);
-                    up = Matrix<T>::mul(vu.v, on.v, up);
-                    down = Matrix<T>::mul(vd.v, on.v, down);
-                }
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    if (up[r] > 0.0f) o[d][r] += INFINITY;
-                    if (down[r] > 0.0f) o[d][r] -= INFINITY;
-                }
+                for (int g = 0; g < NP; ++g) o[d] = Matrix<T>::mul(u.v, p[g], o[d]);
             }
         }
+    }
+    if (odd) {
+        // Key by key, in f32: a value counts where its key is seen.
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+        m = FAR, sum = 0.0f;
+#pragma unroll 1
+        for (int i = i0 + wk; i < i1; i += WK)
+#pragma unroll 1
+            for (int j = key_of(i); j < min(key_of(i) + KT, n); ++j) {
+                const int page = min(max(table[j >> a.page_bits], 0), a.pages - 1), in_page = j & ((1 << a.page_bits) - 1);
+                const T* kr = kc + page * a.k_page + (int64_t)in_page * a.dim;
+                const T* vr = vc + page * a.v_page + (int64_t)in_page * a.dim;
+                float x = 0.0f;
+#pragma unroll
+                for (int t = 0; t < NK; ++t)
+                    if (8 * (2 * t + half) < a.dim) {
+                        const x8 kv = *reinterpret_cast<const x8*>(kr + 8 * (2 * t + half));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x += (float)kv[e] * (float)qt[t][e];
+                    }
+                x = half_sum(x);
+                x = a.cap > 0.0f ? capped<true>(x, a.cap, a.cap_scale) : x * a.scale;
+                const int at = key_position(j);
+                if (a.slopes) x -= a.slopes[head] * LOG2E * fabsf((float)(position - at));
+                if (!(seen_from(j) & 1) || (a.tree && at < from)) continue;
+                const float next = fmaxf(m, x), shrink = __builtin_amdgcn_exp2f(m - next);
+                const float p = __builtin_amdgcn_exp2f(x - next);
+                m = next;
+                sum = sum * shrink + p;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int row = 32 * d + 8 * (r >> 2) + 4 * half + (r & 3);
+                        o[d][r] = o[d][r] * shrink + (row < a.dim ? p * (float)vr[row] : 0.0f);
+                    }
+            }
+        m += (float)Matrix<T>::LIFT;
+        sum = half == 0 ? sum : 0.0f;                  // both halves have it whole
     }
     m -= (float)Matrix<T>::LIFT;                       // sum and o are of powers relative to this
     sum = half_sum(sum);
@@ -609,16 +649,15 @@ hipError_t qpg_launch_cache_attention(const qpg_cache& cache, const qpg_batch& b
     while ((1 << page_bits) < cache.page) ++page_bits;
     const int64_t length = batch.width * cache.page, rows = batch.T * heads, slots = batch.T * group / bc + batch.B;
     const int splits = qpg_cache_attention_splits(batch.T, batch.B, heads, cache.heads, cache.dim, length);
-    constexpr float LOG2E = 1.4426950408889634f;
-    const bool capped = scores.cap > 0.0f;
+    const bool cap = scores.cap > 0.0f;
     AttentionArgs a = {{batch.table, batch.lens, batch.offsets, (int)batch.B, (int)batch.width, (int)batch.T},
                        q, cache.k, cache.v, y, static_cast<float*>(ws),
                        reinterpret_cast<floatx2*>(static_cast<float*>(ws) + (splits > 1 ? splits * rows * cache.dim : 0)),
                        cache.k_stride, cache.v_stride, (int)cache.pages, page_bits, (int)cache.dim, (int)heads,
                        (int)cache.heads, (int)group, (int)slots, splits, y_type,
-                       scores.scale * LOG2E, capped ? scores.cap * LOG2E : 0.0f,
-                       capped ? 2.0f * scores.scale / scores.cap * LOG2E : 0.0f, scores.slopes,
-                       scores.window > 0 && scores.window < 1 << 30 ? (int)scores.window : 1 << 30, scores.prefix, tree,
+                       scores.scale * LOG2E, cap ? scores.cap * LOG2E : 0.0f,
+                       cap ? 2.0f * scores.scale / scores.cap * LOG2E : 0.0f, scores.slopes,
+                       scores.window > 0 && scores.window < NO_WINDOW ? (int)scores.window : NO_WINDOW, scores.prefix, tree,
                        positions, (int)words};
     const bool fine = y_type == QPG_F32 || (y_type == QPG_F16 && cache.type == QPG_BF16);
     const dim3 grid((unsigned)(slots * cache.heads * splits));
