@@ -231,7 +231,9 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     // Loads of a stage: block j of 16 rows of this wave, by its page.
     const T* kc = static_cast<const T*>(a.k) + ((int64_t)h << a.page_bits) * a.dim;
     const T* vc = static_cast<const T*>(a.v) + ((int64_t)h << a.page_bits) * a.dim;
-    const int32_t* table = a.batch.table + (int64_t)b * a.batch.width;
+    // Scalar loads: a vector load's wait would be one for the stage under way as well.
+    typedef __attribute__((address_space(4))) const int32_t uniform_int;
+    uniform_int* table = (uniform_int*)(a.batch.table + (int64_t)b * a.batch.width);
     const int row_bytes = a.dim * 2;
     unsigned voff[LOADS];                              // from the first row of its block
 #pragma unroll
@@ -274,6 +276,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     // The first seen key position of this column, the position of a key, and the seen ones of keys j .. j + 63 as bits
     // (of nodes without the window).
     const int from = a.window < NO_WINDOW ? position - a.window + 1 : -1;
+    const float slope = a.slopes ? a.slopes[head] * LOG2E : 0.0f;
     auto key_position = [&](int j) {
         return a.tree && j >= ctx ? position_of(min(j - ctx, news - 1)) : j;
     };
@@ -310,6 +313,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         load_stage(i0 + wk, 0);
         look_up(i0 + wk + WK);
     }
+    __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0): the loop starts with no load of the compiler's under way
     for (int round = 0; round < rounds; ++round) {
         const int i = i0 + wk + round * WK, buffer = round & 1;
         // this stage has landed, and every wave is done with the other buffer
@@ -333,11 +337,25 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         for (int e = 0; e < NS; ++e)
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[e][r] = 0.0f;
+        // A block's operands are read while the block before it is multiplied.
+        auto keys = [&](int e, int t) { return *reinterpret_cast<const x8*>(kb + e * 32 * DP * 2 + (k_place ^ (t << 5))); };
+        x8 kf[NK];
 #pragma unroll
-        for (int t = 0; t < NK; ++t)
+        for (int t = 0; t < NK; ++t) kf[t] = keys(0, t);
 #pragma unroll
-            for (int e = 0; e < NS; ++e)
-                s[e] = Matrix<T>::mul(*reinterpret_cast<const x8*>(kb + e * 32 * DP * 2 + (k_place ^ (t << 5))), qt[t], s[e]);
+        for (int e = 0; e < NS; ++e)
+#pragma unroll
+            for (int t = 0; t < NK; ++t) {
+                s[e] = Matrix<T>::mul(kf[t], qt[t], s[e]);
+                if (e + 1 < NS) kf[t] = keys(e + 1, t);
+            }
+        __builtin_amdgcn_sched_group_barrier(0x100, NK, 0);             // LDS reads
+#pragma unroll
+        for (int t = 0; t < (NS - 1) * NK; ++t) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // matrix
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, NK, 0);
 
         // Scores in powers of two: c * s once cap and bias are in.
         float c = a.scale;
@@ -356,14 +374,14 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
             const int at_lane = placed ? key_position(key + lane) : 0;
             uint64_t seen = seen_from(key);
             if (a.slopes) {
-                const float slope = -a.slopes[head] * LOG2E, gap = (float)(position - key - 4 * half);
+                const float gap = (float)(position - key - 4 * half);
 #pragma unroll
                 for (int e = 0; e < NS; ++e)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const int i = 32 * e + 8 * (r >> 2) + (r & 3);
                         const float far = placed ? (float)(position - __shfl(at_lane, i + 4 * half)) : gap - (float)i;
-                        s[e][r] = __builtin_fmaf(slope, fabsf(far), s[e][r] * c);
+                        s[e][r] = __builtin_fmaf(-slope, fabsf(far), s[e][r] * c);
                     }
                 c = 1.0f;
             }
@@ -416,23 +434,26 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[d][r] *= shrink;
         }
+        // V^T rows 32d .. 32d + 31, keys 16f + 4 half + 0..3 and + 8
+        auto values = [&](int f, int d) {
+            union { shortx4 s[2]; x8 v; } u;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)(vb + f * 16 * DP * 2 + (v_place[e] ^ (d << 6))));
+            return u.v;
+        };
+        x8 vf[ND];
+#pragma unroll
+        for (int d = 0; d < ND; ++d) vf[d] = values(0, d);
         const float base = (float)Matrix<T>::LIFT - m;
         float part = 0.0f;
-#pragma unroll
-        for (int e = 0; e < NS; ++e)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                s[e][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e][r], c, base));
-                part += s[e][r];
-            }
-        sum += part;
-        // V^T rows 32d .. 32d + 31, keys 16f + 4 half + 0..3 and + 8
 #pragma unroll
         for (int f = 0; f < 2 * NS; ++f) {
             x8 p[NP];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float rest = s[f >> 1][8 * (f & 1) + i];
+                float rest = __builtin_amdgcn_exp2f(__builtin_fmaf(s[f >> 1][8 * (f & 1) + i], c, base));
+                part += rest;
 #pragma unroll
                 for (int g = 0; g < NP; ++g) {
                     const T piece = (T)rest;           // to nearest even; the next piece is what it left
@@ -442,14 +463,12 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
             }
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                union { shortx4 s[2]; x8 v; } u;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)(vb + f * 16 * DP * 2 + (v_place[e] ^ (d << 6))));
-#pragma unroll
-                for (int g = 0; g < NP; ++g) o[d] = Matrix<T>::mul(u.v, p[g], o[d]);
+                for (int g = 0; g < NP; ++g) o[d] = Matrix<T>::mul(vf[d], p[g], o[d]);
+                if (f + 1 < 2 * NS) vf[d] = values(f + 1, d);
             }
         }
+        sum += part;
     }
     if (odd) {
         // Key by key, in f32: a value counts where its key is seen.
@@ -476,7 +495,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
                 x = half_sum(x);
                 x = a.cap > 0.0f ? capped<true>(x, a.cap, a.cap_scale) : x * a.scale;
                 const int at = key_position(j);
-                if (a.slopes) x -= a.slopes[head] * LOG2E * fabsf((float)(position - at));
+                if (a.slopes) x -= slope * fabsf((float)(position - at));
                 if (!(seen_from(j) & 1) || (a.tree && at < from)) continue;
                 const float next = fmaxf(m, x), shrink = __builtin_amdgcn_exp2f(m - next);
                 const float p = __builtin_amdgcn_exp2f(x - next);
