@@ -33,7 +33,7 @@ struct AttentionArgs {
     float* part_o;                // [splits][T * heads][dim]
     floatx2* part_ml;             // [splits][T * heads]: maximum (of scores in powers of two), sum
     int64_t k_page, v_page;       // elements from page to page
-    int pages, page_bits, dim, heads, kv, group, slots, splits, y_type;
+    int pages, page_bits, dim, heads, kv, group, slots, splits, least, y_type;
     float scale, cap;             // scale * log2(e); cap * log2(e) with cap_scale = 2 scale / cap * log2(e)
     float cap_scale;
     const float* slopes;
@@ -98,6 +98,13 @@ __device__ __forceinline__ float half_sum(float x)
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// n / d for 0 <= n < 2^24, 1 <= d: f32's quotient is off by one at most.
+__device__ __forceinline__ int divide(int n, int d)
+{
+    const int q = (int)((float)n * __builtin_amdgcn_rcpf((float)d)), r = n - q * d;
+    return r < 0 ? q - 1 : r >= d ? q + 1 : q;
+}
+
 constexpr int NO_WINDOW = 1 << 30;
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -130,6 +137,7 @@ struct AttentionLds {
     uint8_t v[WK][2][STAGE];
 };
 
+constexpr float DONE = -1.0f;                  // in place of a row's sum where its tile had no second piece
 constexpr float FAR = -3.402823466e38f;        // in place of a maximum of nothing: finite, so differences are numbers
 
 // T: cache type; DP: dim rounded up to 64, 128, 256; WC waves of 32 columns each share a stage of KT
@@ -152,31 +160,51 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     // Head, slot, split of this workgroup: where the heads are a multiple of the eight dies, a
     // head's tiles run on one of them and share its cache; tiles with the most keys first.
     int unit = blockIdx.x, h;
-    const int per_head = a.slots * a.splits;
     if (a.kv % 8 == 0) {
-        h = (unit & 7) + 8 * ((unit >> 3) / per_head);
-        unit = (unit >> 3) % per_head;
+        const int per_head = a.slots * a.splits, q = divide(unit >> 3, per_head);
+        h = (unit & 7) + 8 * q;
+        unit = (unit >> 3) - q * per_head;
     } else {
-        h = unit % a.kv;
-        unit = unit / a.kv;
+        const int q = divide(unit, a.kv);
+        h = unit - q * a.kv;
+        unit = q;
     }
-    const int split = unit % a.splits, slot = a.slots - 1 - unit / a.splits;
+    const int slot = a.slots - 1 - divide(unit, a.splits), split = unit - (a.slots - 1 - slot) * a.splits;
 
-    // Sequence b has slots first(b) .. first(b + 1): enough for its tiles wherever its rows begin.
-    auto first = [&](int i) { return (int64_t)a.batch.offset(i) * a.group / BC + i; };
-    const int b = last_not_above(a.batch.B, slot, first);
-    const int row0 = __builtin_amdgcn_readfirstlane(a.batch.offset(b));
-    const int news = __builtin_amdgcn_readfirstlane(a.batch.offset(b + 1)) - row0;
-    const int64_t tile0 = ((int64_t)slot - first(b)) * BC;
+    // Sequence b has slots first(b) .. first(b + 1): enough for its tiles wherever its rows begin. Its numbers come
+    // with those it is found by where there are few sequences, since each round of loads is time in which nothing
+    // else happens.
+    typedef __attribute__((address_space(4))) const int32_t uniform_int;
+    auto clamped = [&](int at) { return min(max(at, 0), a.batch.T); };
+    auto first = [&](int at, int i) { return (int64_t)at * a.group / BC + i; };
+    int b = 0, row0, row1, n;
+    if (a.batch.B > 1 && a.batch.B < 64) {
+        const int at = clamped(a.batch.offsets[min(lane, a.batch.B)]), length = a.batch.lens[min(lane, a.batch.B - 1)];
+        const uint64_t hit = __ballot(lane < a.batch.B && first(at, lane) <= slot);
+        b = hit ? 63 - __builtin_clzll(hit) : 0;
+        row0 = __builtin_amdgcn_readlane(at, b);
+        row1 = __builtin_amdgcn_readlane(at, b + 1);
+        n = __builtin_amdgcn_readlane(length, b);
+    } else {
+        if (a.batch.B > 1) b = last_not_above(a.batch.B, slot, [&](int i) { return first(a.batch.offset(i), i); });
+        const uniform_int* offsets = (const uniform_int*)a.batch.offsets;
+        row0 = clamped(offsets[b]);
+        row1 = clamped(offsets[b + 1]);
+        n = ((const uniform_int*)a.batch.lens)[b];
+    }
+    const int news = row1 - row0;
+    const int64_t tile0 = (slot - first(row0, b)) * BC;
     if (tile0 < 0 || tile0 >= (int64_t)news * a.group) return;      // the same for the whole workgroup
     const int c0 = (int)tile0, columns = min(BC, news * a.group - c0);
-    const int n = min(max(__builtin_amdgcn_readfirstlane(a.batch.lens[b]), 0), a.batch.width << a.page_bits);
+    n = min(max(n, 0), a.batch.width << a.page_bits);
     const int ctx = n - news;                          // below 0: the first rows have no place
-    const int prefix = a.prefix ? min(max(__builtin_amdgcn_readfirstlane(a.prefix[b]), 0), n) : 0;
+    const int prefix = a.prefix ? min(max(((const uniform_int*)a.prefix)[b], 0), n) : 0;
 
     // This lane's column. Columns behind the last do as the last does, and are not written.
-    const int col = 32 * wc + l31, own = c0 + min(col, columns - 1);
-    const int token = own / a.group, head = h * a.group + own % a.group;
+    const int token0 = c0 / a.group, spare = c0 - token0 * a.group;         // columns are token * group + head in group
+    auto token_of = [&](int i) { return token0 + divide(spare + i, a.group); };
+    const int col = 32 * wc + l31, own = min(col, columns - 1);
+    const int token = token_of(own), head = h * a.group + spare + own - (token - token0) * a.group;
     auto position_of = [&](int t) {
         return a.tree ? min(max(a.positions[row0 + t], 0), 1 << 30) : ctx + t;
     };
@@ -186,7 +214,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     if (a.tree) {
         low = 1 << 30, high = 0;
         if (a.window < NO_WINDOW)
-            for (int t = c0 / a.group + lane; t <= (c0 + columns - 1) / a.group; t += 64) {
+            for (int t = token0 + lane; t <= token_of(columns - 1); t += 64) {
                 low = min(low, position_of(t));
                 high = max(high, position_of(t));
             }
@@ -198,10 +226,10 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         low = wave_low = __builtin_amdgcn_readfirstlane(low);
         high = wave_high = __builtin_amdgcn_readfirstlane(high);
     } else {
-        low = ctx + c0 / a.group;
-        high = ctx + (c0 + columns - 1) / a.group;
-        wave_low = ctx + (c0 + min(32 * wc, columns - 1)) / a.group;
-        wave_high = ctx + (c0 + min(32 * wc + 31, columns - 1)) / a.group;
+        low = ctx + token0;
+        high = ctx + __builtin_amdgcn_readfirstlane(token_of(columns - 1));
+        wave_low = ctx + __builtin_amdgcn_readfirstlane(token_of(min(32 * wc, columns - 1)));
+        wave_high = ctx + __builtin_amdgcn_readfirstlane(token_of(min(32 * wc + 31, columns - 1)));
     }
     // Positions are at most 2^30 and windows are clamped to it: no difference here overflows.
     const int begin = a.window < NO_WINDOW ? max(low - a.window + 1, 0) : 0;
@@ -211,8 +239,10 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     const int begin_stage = max(begin / KT, head_stages), end_stage = (end + KT - 1) / KT;
     const int stages = head_stages + max(end_stage - begin_stage, 0);
     auto key_of = [&](int i) { return (i < head_stages ? i : i - head_stages + begin_stage) * KT; };
-    const int share = ((stages + a.splits - 1) / a.splits + WK - 1) / WK * WK;
+    const int share = max((divide(stages + a.splits - 1, a.splits) + WK - 1) / WK * WK, WK * a.least);
     const int i0 = min(split * share, stages), i1 = min(i0 + share, stages);
+    const bool parts = stages > share;                 // else the first piece is all, and writes y
+    if (!parts && split > 0) return;
     const int rounds = (i1 - i0 + WK - 1) / WK;
 
     // Columns of Q^T: 8 values of 16-byte piece 2t + half.
@@ -232,8 +262,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     const T* kc = static_cast<const T*>(a.k) + ((int64_t)h << a.page_bits) * a.dim;
     const T* vc = static_cast<const T*>(a.v) + ((int64_t)h << a.page_bits) * a.dim;
     // Scalar loads: a vector load's wait would be one for the stage under way as well.
-    typedef __attribute__((address_space(4))) const int32_t uniform_int;
-    uniform_int* table = (uniform_int*)(a.batch.table + (int64_t)b * a.batch.width);
+    const uniform_int* table = (const uniform_int*)(a.batch.table + (int64_t)b * a.batch.width);
     const int row_bytes = a.dim * 2;
     unsigned voff[LOADS];                              // from the first row of its block
 #pragma unroll
@@ -368,24 +397,24 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         }
         const bool whole = a.tree ? last < ctx && (a.window >= NO_WINDOW || high - key < a.window)
                                   : last < n && (last < prefix || (last <= wave_low && wave_high - key < a.window));
-        if (a.slopes || !whole) {
-            // Bit i of `seen`: key + i is seen. Node positions, where they matter, are fetched by the lanes together.
-            const bool placed = a.tree && last >= ctx && (a.slopes || a.window < NO_WINDOW);
-            const int at_lane = placed ? key_position(key + lane) : 0;
-            uint64_t seen = seen_from(key);
-            if (a.slopes) {
-                const float gap = (float)(position - key - 4 * half);
+        // Node positions, where they matter, are fetched by the lanes together.
+        const bool placed = a.tree && last >= ctx && (a.slopes || a.window < NO_WINDOW);
+        const int at_lane = placed ? key_position(key + lane) : 0;
+        if (a.slopes) {
+            const float gap = (float)(position - key - 4 * half);
 #pragma unroll
-                for (int e = 0; e < NS; ++e)
+            for (int e = 0; e < NS; ++e)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int i = 32 * e + 8 * (r >> 2) + (r & 3);
-                        const float far = placed ? (float)(position - __shfl(at_lane, i + 4 * half)) : gap - (float)i;
-                        s[e][r] = __builtin_fmaf(-slope, fabsf(far), s[e][r] * c);
-                    }
-                c = 1.0f;
-            }
-            seen >>= 4 * half;
+                for (int r = 0; r < 16; ++r) {
+                    const int i = 32 * e + 8 * (r >> 2) + (r & 3);
+                    float far = gap - (float)i;
+                    if (placed) far = (float)(position - __shfl(at_lane, i + 4 * half));
+                    s[e][r] = __builtin_fmaf(-slope, fabsf(far), s[e][r] * c);
+                }
+            c = 1.0f;
+        }
+        if (!whole) {
+            const uint64_t seen = seen_from(key) >> (4 * half);        // bit i: key + 4 half + i is seen
 #pragma unroll
             for (int e = 0; e < NS; ++e) {
                 const uint32_t bits = (uint32_t)(seen >> (32 * e));
@@ -564,9 +593,8 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
 
     if (col >= columns) return;
     const int64_t row = (int64_t)(row0 + token) * a.heads + head;
-    const bool parts = a.splits > 1;
     const int64_t part_row = (int64_t)split * a.batch.T * a.heads + row;
-    if (parts && half == 0 && wk == 0) a.part_ml[part_row] = floatx2{m, sum};
+    if (a.splits > 1 && half == 0 && wk == 0) a.part_ml[part_row] = floatx2{m, parts ? sum : DONE};
     if (parts && rounds == 0) return;
     const float inv = parts ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -605,6 +633,7 @@ __global__ void __launch_bounds__(256) cache_attention_join_kernel(const float* 
     if (row >= rows) return;
     const int t = (int)(row / heads), at = (int)(i % fours) * 4;
     if (t < batch.offset(0) || t >= batch.offset(batch.B)) return;
+    if (part_ml[row][1] == DONE) return;
     float m = FAR;
     for (int s = 0; s < splits; ++s) {
         const floatx2 x = part_ml[s * rows + row];
@@ -641,6 +670,8 @@ int tile_columns(int64_t T, int64_t B, int64_t group)
 
 }  // namespace
 
+constexpr int LEAST_STAGES = 2;    // of a group of waves, in a piece
+
 int qpg_cache_attention_splits(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length)
 {
     const int64_t group = heads / kv, bc = tile_columns(T, B, group);
@@ -673,7 +704,7 @@ hipError_t qpg_launch_cache_attention(const qpg_cache& cache, const qpg_batch& b
                        q, cache.k, cache.v, y, static_cast<float*>(ws),
                        reinterpret_cast<floatx2*>(static_cast<float*>(ws) + (splits > 1 ? splits * rows * cache.dim : 0)),
                        cache.k_stride, cache.v_stride, (int)cache.pages, page_bits, (int)cache.dim, (int)heads,
-                       (int)cache.heads, (int)group, (int)slots, splits, y_type,
+                       (int)cache.heads, (int)group, (int)slots, splits, LEAST_STAGES, y_type,
                        scores.scale * LOG2E, cap ? scores.cap * LOG2E : 0.0f,
                        cap ? 2.0f * scores.scale / scores.cap * LOG2E : 0.0f, scores.slopes,
                        scores.window > 0 && scores.window < NO_WINDOW ? (int)scores.window : NO_WINDOW, scores.prefix, tree,
