@@ -54,6 +54,11 @@ template <> struct Matrix<_Float16> {
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
     }
+    static __device__ __forceinline__ float sum2(x8 a, int i, float c)
+    {
+        typedef _Float16 x2 __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2(x2{a[2 * i], a[2 * i + 1]}, x2{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+    }
 };
 template <> struct Matrix<__bf16> {
     typedef bf16x8 x8;
@@ -64,15 +69,23 @@ template <> struct Matrix<__bf16> {
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
+    static __device__ __forceinline__ float sum2(x8 a, int i, float c)
+    {
+        typedef __bf16 x2 __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2_f32_bf16(x2{a[2 * i], a[2 * i + 1]}, x2{(__bf16)1.0f, (__bf16)1.0f}, c, false);
+    }
 };
 
 // Each lane's 16 bytes at voff go to LDS byte lds_wave_base + 16 * lane. Inline asm, so that the
 // compiler's own waits leave the prefetch alone; the kernel waits before a stage is read. m0
 // carries the wave-uniform LDS address. The compiler does not look into the asm: five wait states, since
 // its scalar operands may come straight from a lane (v_readlane, v_readfirstlane).
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, unsigned lds_wave_base, unsigned voff)
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, unsigned lds_wave_base, unsigned voff, bool fresh)
 {
-    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(r), "{m0}"(lds_wave_base) : "memory");
+    if (!fresh)
+        asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(r), "{m0}"(lds_wave_base) : "memory");
+    else
+        asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(r), "{m0}"(lds_wave_base) : "memory");
 }
 
 // A descriptor of `bytes` bytes from p, both the same for the wave.
@@ -289,8 +302,10 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
             const int there = min(max(n - first_key, 0), 16) * row_bytes;
             const int page = pages[NB == 1 ? 0 : (j * RPI) / 16];
             const int64_t in_block = (int64_t)in_page * a.dim;
-            load_to_lds(buffer_of(kc + page * a.k_page + in_block, there), lds_k + buffer * STAGE + row * DP * 2, voff[j]);
-            load_to_lds(buffer_of(vc + page * a.v_page + in_block, there), lds_v + buffer * STAGE + row * DP * 2, voff[j]);
+            load_to_lds(buffer_of(kc + page * a.k_page + in_block, there), lds_k + buffer * STAGE + row * DP * 2, voff[j],
+                        j * RPI % 16 == 0);
+            load_to_lds(buffer_of(vc + page * a.v_page + in_block, there), lds_v + buffer * STAGE + row * DP * 2, voff[j],
+                        j * RPI % 16 == 0);
         }
     };
 
@@ -342,7 +357,13 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         load_stage(i0 + wk, 0);
         look_up(i0 + wk + WK);
     }
-    __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0): the loop starts with no load of the compiler's under way
+    // The compiler's own loads end here, so that none of its waits in the loop is one for the stage under way.
+#pragma unroll
+    for (int t = 0; t < NK; ++t) asm volatile("" : "+v"(qt[t]));
+    // Stages whose keys every column of the wave sees, and whose scores are the products, take a short way.
+    int plain_low = a.window < NO_WINDOW ? wave_high - a.window + 1 : 0, plain_high = min(wave_low, n - 1);
+    if (a.tree) plain_low = a.window < NO_WINDOW ? high - a.window + 1 : 0, plain_high = min(ctx, n) - 1;
+    if (a.slopes || a.cap > 0.0f) plain_high = -1;
     for (int round = 0; round < rounds; ++round) {
         const int i = i0 + wk + round * WK, buffer = round & 1;
         // this stage has landed, and every wave is done with the other buffer
@@ -386,64 +407,69 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         }
         __builtin_amdgcn_sched_group_barrier(0x008, NK, 0);
 
-        // Scores in powers of two: c * s once cap and bias are in.
-        float c = a.scale;
-        if (a.cap > 0.0f) {
-            c = 1.0f;
+        float c = a.scale;                             // c * s are scores in powers of two
+        if (key < plain_low || last > plain_high) {
+            if (a.cap > 0.0f) {
+                c = 1.0f;
 #pragma unroll
-            for (int e = 0; e < NS; ++e)
+                for (int e = 0; e < NS; ++e)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[e][r] = capped<(NP > 1)>(s[e][r], a.cap, a.cap_scale);
-        }
-        const bool whole = a.tree ? last < ctx && (a.window >= NO_WINDOW || high - key < a.window)
-                                  : last < n && (last < prefix || (last <= wave_low && wave_high - key < a.window));
-        // Node positions, where they matter, are fetched by the lanes together.
-        const bool placed = a.tree && last >= ctx && (a.slopes || a.window < NO_WINDOW);
-        const int at_lane = placed ? key_position(key + lane) : 0;
-        if (a.slopes) {
-            const float gap = (float)(position - key - 4 * half);
-#pragma unroll
-            for (int e = 0; e < NS; ++e)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int i = 32 * e + 8 * (r >> 2) + (r & 3);
-                    float far = gap - (float)i;
-                    if (placed) far = (float)(position - __shfl(at_lane, i + 4 * half));
-                    s[e][r] = __builtin_fmaf(-slope, fabsf(far), s[e][r] * c);
-                }
-            c = 1.0f;
-        }
-        if (!whole) {
-            const uint64_t seen = seen_from(key) >> (4 * half);        // bit i: key + 4 half + i is seen
-#pragma unroll
-            for (int e = 0; e < NS; ++e) {
-                const uint32_t bits = (uint32_t)(seen >> (32 * e));
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int i = 8 * (r >> 2) + (r & 3);
-                    bool on = (bits >> i) & 1;
-                    if (placed) {
-                        const int at = __shfl(at_lane, 32 * e + i + 4 * half);         // by all lanes
-                        on = on && at >= from;
-                    }
-                    s[e][r] = on ? s[e][r] : -INFINITY;
-                }
+                    for (int r = 0; r < 16; ++r) s[e][r] = capped<(NP > 1)>(s[e][r], a.cap, a.cap_scale);
             }
-            // A value that is no number times a share of 0 would be NaN. Rows that one column of the wave sees and
-            // another does not are looked through for such values; where there are any, the columns are done again below.
-            const int upto = min(last, n - 1);
-            const bool mixed = a.tree ? upto >= ctx || high - key >= a.window
-                                      : !(upto < prefix || (upto <= wave_low && wave_high - key < a.window));
-            if (mixed) {
-                ushortx2 most = {0, 0};
-#pragma unroll 4
-                for (int at = lane * 16; at < STAGE; at += 1024) {
-                    const uint32x4 x = *reinterpret_cast<const uint32x4*>(vb + at);
+            const bool whole = a.tree ? last < ctx && (a.window >= NO_WINDOW || high - key < a.window)
+                                      : last < n && (last < prefix || (last <= wave_low && wave_high - key < a.window));
+            // Node positions, where they matter, are fetched by the lanes together.
+            const bool placed = a.tree && last >= ctx && (a.slopes || a.window < NO_WINDOW);
+            int at_lane = 0;
+            if (placed) {
+                at_lane = key_position(key + lane);
+                asm volatile("" : "+v"(at_lane));          // its load ends here
+            }
+            if (a.slopes) {
+                const float gap = (float)(position - key - 4 * half);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        most = __builtin_elementwise_max(most, __builtin_bit_cast(ushortx2, x[e] & 0x7FFF7FFFu));
+                for (int e = 0; e < NS; ++e)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int i = 32 * e + 8 * (r >> 2) + (r & 3);
+                        float far = gap - (float)i;
+                        if (placed) far = (float)(position - __shfl(at_lane, i + 4 * half));
+                        s[e][r] = __builtin_fmaf(-slope, fabsf(far), s[e][r] * c);
+                    }
+                c = 1.0f;
+            }
+            if (!whole) {
+                const uint64_t seen = seen_from(key) >> (4 * half);        // bit i: key + 4 half + i is seen
+#pragma unroll
+                for (int e = 0; e < NS; ++e) {
+                    const uint32_t bits = (uint32_t)(seen >> (32 * e));
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int i = 8 * (r >> 2) + (r & 3);
+                        bool on = (bits >> i) & 1;
+                        if (placed) {
+                            const int at = __shfl(at_lane, 32 * e + i + 4 * half);         // by all lanes
+                            on = on && at >= from;
+                        }
+                        s[e][r] = on ? s[e][r] : -INFINITY;
+                    }
                 }
-                odd |= __ballot(max(most[0], most[1]) >= Matrix<T>::INF) != 0;
+                // A value that is no number times a share of 0 would be NaN. Rows that one column of the wave sees and
+                // another does not are looked through for such values; where there are any, the columns are done again below.
+                const int upto = min(last, n - 1);
+                const bool mixed = a.tree ? upto >= ctx || high - key >= a.window
+                                          : !(upto < prefix || (upto <= wave_low && wave_high - key < a.window));
+                if (mixed) {
+                    ushortx2 most = {0, 0};
+#pragma unroll 4
+                    for (int at = lane * 16; at < STAGE; at += 1024) {
+                        const uint32x4 x = *reinterpret_cast<const uint32x4*>(vb + at);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            most = __builtin_elementwise_max(most, __builtin_bit_cast(ushortx2, x[e] & 0x7FFF7FFFu));
+                    }
+                    odd |= __ballot(max(most[0], most[1]) >= Matrix<T>::INF) != 0;
+                }
             }
         }
 
@@ -482,7 +508,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float rest = __builtin_amdgcn_exp2f(__builtin_fmaf(s[f >> 1][8 * (f & 1) + i], c, base));
-                part += rest;
+                if (NP > 1) part += rest;
 #pragma unroll
                 for (int g = 0; g < NP; ++g) {
                     const T piece = (T)rest;           // to nearest even; the next piece is what it left
@@ -490,6 +516,9 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
                     rest -= (float)piece;
                 }
             }
+            if (NP == 1)                               // the sum of the shares as they are multiplied, two at a time
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part = Matrix<T>::sum2(p[0], i, part);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
 #pragma unroll
