@@ -690,32 +690,68 @@ __global__ void __launch_bounds__(256) cache_attention_join_kernel(const float* 
 
 namespace {
 
-// Columns of a tile, by the columns that a sequence has on average.
-int tile_columns(int64_t T, int64_t B, int64_t group)
-{
-    const int64_t mean = (T * group + B - 1) / B;
-    return mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
-}
+// How a call is laid over the card: WC * 32 columns to a tile, WK groups of waves, keys in `splits` pieces.
+struct AttentionForm {
+    int wc, wk, splits;
+    int64_t slots;
+};
 
-}  // namespace
+// Chosen by what the host knows: the mean number of columns and the longest length that the table holds. Both sides
+// measured (us, heads of 128 unless said; MHA: 32 of 32 heads, GQA: 32 of 8):
+//   tiles of 128 where they are 256 and more, shared by two groups of waves up to 1024 of them: prompts of 1024 to
+//     4096 tokens MHA 35, 72, 172 against 43, 74, 185 by one group; of 8192 GQA, 2048 tiles, 581 against 542
+//   else tiles of 64 where they are 192 and more (512 tokens MHA 16.0; tiles of 128 19.5, of 32 22.4), and of 32 below
+//     (256 tokens 11.0; of 64 12.9; 26 drafts over 2048 tokens GQA 18.0; of 64 21.1, of 128 22.4)
+//   but not over long caches, where larger tiles in pieces read less: 512 tokens over 8000 GQA 87 against 104 of 64
+//     and 146 of 32; 128 tokens over 8000 39.6 (64, four pieces) against 47.9 (32)
+//   heads of up to 256: tiles of 128 from 512 of them (4096 tokens, 16 of 8 heads: 229, of 64 252; 1024 tokens: of
+//     64 39.7, of 128 51.5)
+//   pieces until there are about 128 workgroups, since joining them costs 4 us and more (one token over 4096, MHA: one
+//     piece 32, four 23.0, eight 23.8), and two where long caches would leave CUs without work at the end
+//     (64 tokens over up to 8100 GQA: 230, 197 with two). A piece has at least 256 keys.
+AttentionForm form_of(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length)
+{
+    const int64_t group = heads / kv, busy = B < T ? B : T, mean = (T * group + busy - 1) / busy;
+    auto tiles = [&](int64_t columns) { return busy * ((mean + columns - 1) / columns) * kv; };
+    const bool wide = dim > 128, far = length >= 4096;
+    AttentionForm f;
+    if (mean > 64 && tiles(128) >= (wide ? 512 : 256)) {
+        f.wc = 4;
+        f.wk = !wide && tiles(128) <= 1024 ? 2 : 1;
+    } else if (mean > 64 && !wide && far && tiles(128) * length >= 512 * 1024) {
+        f.wc = 4;
+        f.wk = 2;
+    } else if (mean > 32 && (tiles(64) >= (wide ? 128 : 192) || (mean > 64 && far))) {
+        f.wc = 2;
+        f.wk = wide ? 2 : 4;
+    } else {
+        f.wc = 1;
+        f.wk = wide ? 2 : 4;
+    }
+    const int64_t count = tiles(32 * f.wc), goal = f.wc == 1 ? 128 : 256;
+    int64_t splits = (goal + count - 1) / count;
+    if (splits < 2 && far && f.wc == 1 && count <= 1024) splits = 2;
+    if (f.wc > 1 && !far) splits = 1;
+    if (splits > length / 256) splits = length / 256;
+    if (splits > 64) splits = 64;
+    f.splits = splits < 1 ? 1 : (int)splits;
+    f.slots = T * group / (32 * f.wc) + B;
+    return f;
+}
 
 constexpr int LEAST_STAGES = 2;    // of a group of waves, in a piece
 
+}  // namespace
+
 int qpg_cache_attention_splits(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length)
 {
-    const int64_t group = heads / kv, bc = tile_columns(T, B, group);
-    const int64_t tiles = ((T * group + bc - 1) / bc > (B < T ? B : T) ? (T * group + bc - 1) / bc : (B < T ? B : T)) * kv;
-    // pieces of at least 256 keys, and about 1024 workgroups
-    int64_t splits = 1024 / tiles;
-    if (splits > length / 256) splits = length / 256;
-    if (splits > 64) splits = 64;
-    return splits < 1 ? 1 : (int)splits;
+    return form_of(T, B, heads, kv, dim, length).splits;
 }
 
 int64_t qpg_cache_attention_grid(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length)
 {
-    const int64_t group = heads / kv;
-    return (T * group / tile_columns(T, B, group) + B) * kv * qpg_cache_attention_splits(T, B, heads, kv, dim, length);
+    const AttentionForm f = form_of(T, B, heads, kv, dim, length);
+    return f.slots * kv * f.splits;
 }
 
 hipError_t qpg_launch_cache_attention(const qpg_cache& cache, const qpg_batch& batch, const qpg_scores& scores,
@@ -723,11 +759,12 @@ hipError_t qpg_launch_cache_attention(const qpg_cache& cache, const qpg_batch& b
                                       const int32_t* positions, void* y, int y_type, void* ws, hipStream_t s)
 {
     using namespace qpg;
-    const int64_t group = heads / cache.heads, bc = tile_columns(batch.T, batch.B, group);
+    const int64_t group = heads / cache.heads, rows = batch.T * heads;
     int page_bits = 0;
     while ((1 << page_bits) < cache.page) ++page_bits;
-    const int64_t length = batch.width * cache.page, rows = batch.T * heads, slots = batch.T * group / bc + batch.B;
-    const int splits = qpg_cache_attention_splits(batch.T, batch.B, heads, cache.heads, cache.dim, length);
+    const AttentionForm form = form_of(batch.T, batch.B, heads, cache.heads, cache.dim, batch.width * cache.page);
+    const int64_t slots = form.slots;
+    const int splits = form.splits;
     const bool cap = scores.cap > 0.0f;
     AttentionArgs a = {{batch.table, batch.lens, batch.offsets, (int)batch.B, (int)batch.width, (int)batch.T},
                        q, cache.k, cache.v, y, static_cast<float*>(ws),
@@ -751,14 +788,20 @@ hipError_t qpg_launch_cache_attention(const qpg_cache& cache, const qpg_batch& b
     };
     using std::integral_constant;
     auto by_columns = [&](auto t, auto dp) {
-        constexpr int DP = decltype(dp)::value, KT = DP == 256 ? 32 : 64;
-        if (bc == 128) return launch(t, dp, integral_constant<int, 4>(), integral_constant<int, 1>(), integral_constant<int, KT>());
-        if constexpr (DP == 256) {
-            if (bc == 64) return launch(t, dp, integral_constant<int, 2>(), integral_constant<int, 2>(), integral_constant<int, 32>());
-            return launch(t, dp, integral_constant<int, 1>(), integral_constant<int, 2>(), integral_constant<int, 32>());
+        const integral_constant<int, 1> one;
+        const integral_constant<int, 2> two;
+        const integral_constant<int, 4> four;
+        const integral_constant<int, 32> half_stage;
+        const integral_constant<int, 64> stage;
+        if constexpr (decltype(dp)::value == 256) {
+            if (form.wc == 4) return launch(t, dp, four, one, half_stage);
+            if (form.wc == 2) return launch(t, dp, two, two, half_stage);
+            return launch(t, dp, one, two, half_stage);
         } else {
-            if (bc == 64) return launch(t, dp, integral_constant<int, 2>(), integral_constant<int, 2>(), integral_constant<int, 32>());
-            return launch(t, dp, integral_constant<int, 1>(), integral_constant<int, 4>(), integral_constant<int, 32>());
+            if (form.wc == 4 && form.wk == 1) return launch(t, dp, four, one, stage);
+            if (form.wc == 4) return launch(t, dp, four, two, stage);
+            if (form.wc == 2) return launch(t, dp, two, four, half_stage);
+            return launch(t, dp, one, four, half_stage);
         }
     };
     auto by_dim = [&](auto t) {

@@ -301,3 +301,31 @@ def test_graph_replays_with_other_contents():
         check(got[mine], want[mine], bound[mine])
         assert bool((got[~mine] == 777.0).all())
         assert torch.equal(qpg.cache_attention(q, k, v, table, lens, offsets, dtype=torch.float32)[mine.to(DEV)], y[mine.to(DEV)])
+
+
+# Shapes that take each form of the launch (tiles of 32, 64 and 128 columns, one and two groups of waves, one and more
+# pieces): new tokens, lengths, heads, cache heads, dim, page
+FORMS = [([256], [256], 32, 32, 64, 16), ([520], [520], 32, 32, 64, 64), ([520], [600], 32, 8, 128, 64), ([1030], [1030], 32, 32, 64, 64),
+         ([1100], [1100], 32, 8, 128, 128), ([2100], [2100], 64, 64, 64, 256), ([130, 3, 40], [5000, 4200, 60], 16, 4, 128, 64),
+         ([300], [5000], 16, 4, 128, 16), ([520], [4500], 8, 8, 256, 64), ([700], [700], 16, 8, 192, 32), ([2100], [2100], 32, 32, 256, 64),
+         ([1] * 40, [4200] + [i * 3 + 1 for i in range(39)], 16, 4, 128, 64)]
+
+
+@pytest.mark.parametrize("kind,y", [("bf16", "bf16"), ("f16", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("case", FORMS, ids=[f"{sum(c[0])}-{max(c[1])}-{c[2]}-{c[3]}-{c[4]}" for c in FORMS])
+def test_forms(case, kind, y):
+    """Rows here and there of large calls against 64 bits."""
+    new, lens, heads, kv, dim, page = case
+    batch = R.Batch(new, lens, kv, dim, page, kind, seed=len(new))
+    q = batch.normal(batch.rows, heads, dim)
+    got = qpg.cache_attention(q.to(DEV), batch.k.to(DEV), batch.v.to(DEV), *batch.index(DEV), dtype=R.TYPES[y]).cpu().double()
+    group, at = heads // kv, 0
+    for b, (n, length) in enumerate(zip(new, lens)):
+        for h in sorted({0, heads - 1, heads // 2}):
+            one = R.Batch([n], [length], 1, dim, page, kind, seed=0)
+            for c, src in ((one.k, batch.k), (one.v, batch.v)):
+                for p in range(-(-length // page)):
+                    c[one.table[0, p], 0] = src[batch.table[b, p], h // group]
+            want, bound, _ = R.attention(one, q[at:at + n, h:h + 1], y)
+            check(got[at:at + n, h:h + 1], want, bound)
+        at += n
