@@ -398,15 +398,16 @@ def _current_raw_stream(dev: int) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-# 0.1 us where torch has it (a torch built without a GPU backend does not, and still loads this module)
+# 0.1 us where torch has them (a torch built without a GPU backend does not, and still loads this module)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _run(t: torch.Tensor, stream, call):
     """call(raw stream) with t's device current and `stream` (t's device's current one if None)
     the one that torch allocates on."""
     dev = t.get_device()
-    if stream is None and dev == torch.cuda.current_device():
+    if stream is None and dev == _current_device():
         return call(_raw_stream(dev))
     if stream is not None and stream.device != t.device:
         raise QPGError(QPG_EINVAL, f"the stream is on {stream.device}, the operands on {t.device}")
@@ -718,38 +719,44 @@ class _Scores(ctypes.Structure):
 
 def _cache(k: torch.Tensor, v: torch.Tensor):
     """The cache as the library takes it: [pages, heads, page, dim] each, pages any distance apart."""
+    shape, dev = k.shape, k.get_device()
     code = _TYPES.get(k.dtype, 0)
     if code == 0:
         raise QPGError(QPG_EINVAL, f"k_cache must be float16 or bfloat16, got {k.dtype}")
-    shape = k.shape
-    if len(shape) != 4:
-        raise QPGError(QPG_EINVAL, f"k_cache must have 4 dimensions, got {tuple(shape)}")
-    if min(shape) < 1:
-        raise QPGError(QPG_EINVAL, f"k_cache is empty: {tuple(shape)}")
+    if len(shape) != 4 or min(shape) < 1:
+        raise QPGError(QPG_EINVAL, f"k_cache must have 4 dimensions, none empty, got {tuple(shape)}")
     pages, heads, page, dim = shape
-    for t, name in ((k, "k_cache"), (v, "v_cache")):
-        if t.dtype is not k.dtype or t.shape != shape or t.get_device() != k.get_device() or t.get_device() < 0:
+    k_stride = v_stride = heads * page * dim
+    if v.dtype is not k.dtype or v.shape != shape or v.get_device() != dev or dev < 0:
+        for t, name in ((k, "k_cache"), (v, "v_cache")):
             if not t.is_cuda:
                 raise QPGError(QPG_EINVAL, f"{name} must be a device tensor")
-            _same_device(t, k, name)
-            raise QPGError(QPG_EINVAL, f"{name} must be {k.dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-        s = t.stride()
-        # an extent of 1 has no stride to speak of
-        if (dim > 1 and s[3] != 1) or (page > 1 and s[2] != dim) or (heads > 1 and s[1] != page * dim) or \
-                (pages > 1 and s[0] < heads * page * dim):
-            raise QPGError(QPG_EINVAL, f"{name} must be contiguous within a page, strides {s}")
-    block = heads * page * dim
-    return _Cache(k.data_ptr(), v.data_ptr(), code, pages, heads, page, dim, k.stride(0) if pages > 1 else block,
-                  v.stride(0) if pages > 1 else block)
+        _same_device(v, k, "v_cache")
+        raise QPGError(QPG_EINVAL, f"v_cache must be {k.dtype} {tuple(shape)}, got {v.dtype} {tuple(v.shape)}")
+    if not (k.is_contiguous() and v.is_contiguous()):
+        for t, name in ((k, "k_cache"), (v, "v_cache")):
+            s = t.stride()
+            # an extent of 1 has no stride to speak of
+            if (dim > 1 and s[3] != 1) or (page > 1 and s[2] != dim) or (heads > 1 and s[1] != page * dim) or \
+                    (pages > 1 and s[0] < heads * page * dim):
+                raise QPGError(QPG_EINVAL, f"{name} must be contiguous within a page, strides {s}")
+        if pages > 1:
+            k_stride, v_stride = k.stride(0), v.stride(0)
+    return _Cache(k.data_ptr(), v.data_ptr(), code, pages, heads, page, dim, k_stride, v_stride)
 
 
 def _batch(table: torch.Tensor, lens: torch.Tensor, offsets: torch.Tensor, T: int, ref: torch.Tensor):
-    if table.dim() != 2:
-        raise QPGError(QPG_EINVAL, f"table must have 2 dimensions, got {tuple(table.shape)}")
-    B, width = table.shape
-    _is(table, torch.int32, (B, width), "table", ref)
-    _is(lens, torch.int32, (B,), "lens", ref)
-    _is(offsets, torch.int32, (B + 1,), "offsets", ref)
+    shape, dev, i32 = table.shape, ref.get_device(), torch.int32
+    if len(shape) != 2:
+        raise QPGError(QPG_EINVAL, f"table must have 2 dimensions, got {tuple(shape)}")
+    B, width = shape
+    if not (table.dtype is i32 and lens.dtype is i32 and offsets.dtype is i32 and table.get_device() == dev and
+            lens.get_device() == dev and offsets.get_device() == dev and table.is_contiguous() and lens.is_contiguous() and
+            offsets.is_contiguous() and lens.dim() == 1 and offsets.dim() == 1 and lens.numel() == B and
+            offsets.numel() == B + 1):
+        _is(table, i32, (B, width), "table", ref)
+        _is(lens, i32, (B,), "lens", ref)
+        _is(offsets, i32, (B + 1,), "offsets", ref)
     return _Batch(table.data_ptr(), lens.data_ptr(), offsets.data_ptr(), B, width, T)
 
 
@@ -757,8 +764,8 @@ def _at(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _heads(t: torch.Tensor, dim: int, name: str, ref: torch.Tensor) -> int:
-    """Heads of a matrix [T, heads * dim] whose rows are contiguous, any distance apart."""
+def _rows(t: torch.Tensor, like: torch.Tensor, dim: int, name: str, ref: torch.Tensor):
+    """(heads, distance of the rows) of a matrix [T, heads * dim] whose rows are contiguous, of like's type and rows."""
     if t.get_device() != ref.get_device():
         if not t.is_cuda:
             raise QPGError(QPG_EINVAL, f"{name} must be a device tensor")
@@ -768,9 +775,12 @@ def _heads(t: torch.Tensor, dim: int, name: str, ref: torch.Tensor) -> int:
     T, n = t.shape
     if n % dim:
         raise QPGError(QPG_EINVAL, f"{name}: rows of {n} are no heads of {dim}")
-    if (n > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < n):
+    stride, step = t.stride()
+    if (n > 1 and step != 1) or (T > 1 and stride < n):
         raise QPGError(QPG_EINVAL, f"{name} must have contiguous rows, strides {t.stride()}")
-    return n // dim
+    if t.dtype is not like.dtype or T != like.shape[0]:
+        raise QPGError(QPG_EINVAL, f"{name} is {t.dtype} of {T} rows, k {like.dtype} of {like.shape[0]}")
+    return n // dim, stride
 
 
 def cache_append(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
@@ -785,45 +795,40 @@ def cache_append(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     left alone. freqs [rot / 2] float32: a pair of values turns by position * freq (None: no rotation); pairs are
     neighbours (adjacent) or half a rotation apart. positions [T] int32 (None: the place in the sequence).
     q_norm, k_norm [dim] float32: weights of the norm (None: none)."""
-    shape = k_cache.shape
     cache = _cache(k_cache, v_cache)
-    dim, code = cache.dim, _type(k.dtype, "k")
-    heads = 0
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t is None and name == "q":
-            continue
-        n = _heads(t, dim, name, k_cache)
-        if t.dtype is not k.dtype or t.shape[0] != k.shape[0]:
-            raise QPGError(QPG_EINVAL, f"{name} is {t.dtype} of {t.shape[0]} rows, k {k.dtype} of {k.shape[0]}")
-        if name == "q":
-            heads = n
-            if n < 1 or n % shape[1]:
-                raise QPGError(QPG_EINVAL, f"{n} query heads over {shape[1]} heads of the cache")
-        elif n != shape[1]:
-            raise QPGError(QPG_EINVAL, f"{name} has {n} heads, the cache {shape[1]}")
+    dim, kv, code = cache.dim, cache.heads, _type(k.dtype, "k")
+    heads = q_stride = rot = 0
+    k_heads, k_stride = _rows(k, k, dim, "k", k_cache)
+    v_heads, v_stride = _rows(v, k, dim, "v", k_cache)
+    if k_heads != kv or v_heads != kv:
+        raise QPGError(QPG_EINVAL, f"{k_heads} heads of k and {v_heads} of v, the cache has {kv}")
     T = k.shape[0]
+    if q is not None:
+        heads, q_stride = _rows(q, k, dim, "q", k_cache)
+        if heads < 1 or heads % kv:
+            raise QPGError(QPG_EINVAL, f"{heads} query heads over {kv} heads of the cache")
     batch = _batch(table, lens, offsets, T, k_cache)
-    rot = 0
     if freqs is not None:
         rot = 2 * freqs.numel()
         _is(freqs, torch.float32, (rot // 2,), "freqs", k_cache)
     if positions is not None:
         _is(positions, torch.int32, (T,), "positions", k_cache)
-    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None:
-            _is(t, torch.float32, (dim,), name, k_cache)
+    if q_norm is not None:
+        _is(q_norm, torch.float32, (dim,), "q_norm", k_cache)
+    if k_norm is not None:
+        _is(k_norm, torch.float32, (dim,), "k_norm", k_cache)
     if y is not None:
         if q is None:
             raise QPGError(QPG_EINVAL, "y without q")
         _is(y, k_cache.dtype, (T, heads, dim), "y", k_cache)
 
     def call(s):
-        out = y
-        if y is None and heads:
-            out = torch.empty((T, heads, dim), dtype=k_cache.dtype, device=k_cache.device)
-        _check(lib().cache_append(ctypes.byref(cache), ctypes.byref(batch), _at(q), k.data_ptr(), v.data_ptr(), code,
-                                  0 if q is None else q.stride(0), k.stride(0), v.stride(0), heads, _at(positions), _at(freqs),
-                                  rot, bool(adjacent), _at(q_norm), _at(k_norm), eps, _at(out), s), "cache_append")
+        out = k_cache.new_empty((T, heads, dim)) if y is None and heads else y
+        rc = lib().cache_append(ctypes.byref(cache), ctypes.byref(batch), _at(q), k.data_ptr(), v.data_ptr(), code, q_stride,
+                                k_stride, v_stride, heads, _at(positions), _at(freqs), rot, 1 if adjacent else 0, _at(q_norm),
+                                _at(k_norm), eps, _at(out), s)
+        if rc:
+            _check(rc, "cache_append")
         return out
     return _run(k_cache, stream, call)
 
@@ -837,12 +842,15 @@ def cache_attention_bytes(T: int, B: int, heads: int, cache_heads: int, dim: int
 def _attention(q, k_cache, v_cache, table, lens, offsets, scale, cap, slopes, window, prefix, tree, positions, y, ws, dtype,
                stream, what):
     cache = _cache(k_cache, v_cache)
-    if q.dim() != 3:
-        raise QPGError(QPG_EINVAL, f"q must have 3 dimensions, got {tuple(q.shape)}")
-    T, heads, dim = q.shape
-    if dim != cache.dim or heads < 1 or heads % cache.heads:
-        raise QPGError(QPG_EINVAL, f"{heads} query heads of {dim} over {cache.heads} heads of {cache.dim}")
-    _is(q, k_cache.dtype, (T, heads, dim), "q", k_cache)
+    shape = q.shape
+    if len(shape) != 3:
+        raise QPGError(QPG_EINVAL, f"q must have 3 dimensions, got {tuple(shape)}")
+    T, heads, dim = shape
+    kv = cache.heads
+    if dim != cache.dim or heads < 1 or heads % kv:
+        raise QPGError(QPG_EINVAL, f"{heads} query heads of {dim} over {kv} heads of {cache.dim}")
+    if q.dtype is not k_cache.dtype or q.get_device() != k_cache.get_device() or not q.is_contiguous():
+        _is(q, k_cache.dtype, shape, "q", k_cache)
     batch = _batch(table, lens, offsets, T, k_cache)
     if slopes is not None:
         _is(slopes, torch.float32, (heads,), "slopes", k_cache)
@@ -855,21 +863,23 @@ def _attention(q, k_cache, v_cache, table, lens, offsets, scale, cap, slopes, wi
         words = tree.shape[1]
         _is(tree, torch.int64, (T, words), "tree", k_cache)
         _is(positions, torch.int32, (T,), "positions", k_cache)
-    dtype, code = _given(y, q.dtype if dtype is None else dtype, (T, heads, dim), "y", k_cache)
-    nws = cache_attention_bytes(T, batch.B, heads, cache.heads, dim, batch.width * cache.page)
+    dtype, code = _given(y, q.dtype if dtype is None else dtype, shape, "y", k_cache)
+    nws = cache_attention_bytes(T, batch.B, heads, kv, dim, batch.width * cache.page)
     if ws is not None:
         _out(ws, torch.uint8, "ws", nws, k_cache)
     scores = _Scores(1.0 / math.sqrt(dim) if scale is None else scale, cap, _at(slopes), window, _at(prefix))
 
     def call(s):
-        out = torch.empty((T, heads, dim), dtype=dtype, device=q.device) if y is None else y
-        w = torch.empty(nws, dtype=torch.uint8, device=q.device) if ws is None and nws else ws
-        args = ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(scores), q.data_ptr(), heads
+        out = q.new_empty(shape, dtype=dtype) if y is None else y
+        w = q.new_empty(nws, dtype=torch.uint8) if ws is None and nws else ws
         if tree is None:
-            rc = lib().cache_attention(*args, out.data_ptr(), code, _at(w), s)
+            rc = lib().cache_attention(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(scores), q.data_ptr(), heads,
+                                       out.data_ptr(), code, _at(w), s)
         else:
-            rc = lib().cache_attention_tree(*args, tree.data_ptr(), words, positions.data_ptr(), out.data_ptr(), code, _at(w), s)
-        _check(rc, what)
+            rc = lib().cache_attention_tree(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(scores), q.data_ptr(), heads,
+                                            tree.data_ptr(), words, positions.data_ptr(), out.data_ptr(), code, _at(w), s)
+        if rc:
+            _check(rc, what)
         return out
     return _run(k_cache, stream, call)
 
