@@ -13,6 +13,7 @@ Other modes:
                              points (one JSON line per shape)
   --msweep                   the 7B layer GEMM shapes at M = 16 .. 2048 tokens, likewise
   --experts                  the 7B-shaped stack with 8 MXFP4 experts, two to a token, for its FFN
+  --attention                the 7B-shaped stack with attention over paged caches: prompt, decoding, drafts
                              (one JSON line)
   --q6forms                  the raw, prepared and expanded q6_K forms on the v and down
                              shapes at M = 16 .. 1024, likewise
@@ -526,6 +527,60 @@ def run_experts(steps: int, warmup: int, layers: int = 4, M: int = 1024, E: int 
                       "gate_tflops": round(gate / us["gate"] / 1e6, 1), "data": "synthetic"}), flush=True)
 
 
+def run_attention(steps: int, warmup: int, layers: int = 4, page: int = 64):
+    """The stack with attention over paged caches as one HIP graph per pass: a prompt of 1024 tokens, 64 tokens being
+    decoded over 2048 each, and 8 trees of 32 drafts over 2048. Of each the pass with and without (mode
+    gemm) and one layer's attention: HIP events around `steps` passes, five rounds, medians."""
+    import statistics
+    import torch
+    from quantized_prefill_gemm_amd import inputs
+    from quantized_prefill_gemm_amd.stack import AttentionStack
+    dev = torch.device("cuda:0")
+    gen = torch.Generator(device=dev).manual_seed(inputs.BASE_SEED + 7)
+    weights = [[torch.from_numpy(inputs.make_stack_matrix(layer, idx)[4].reshape(-1)).to(dev)
+                for idx in range(len(inputs.STACK_LAYER))] for layer in range(layers)]
+
+    def timed(fn):
+        for _ in range(warmup):
+            fn()
+        t = []
+        for _ in range(ROUNDS):
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            e0.record()
+            for _ in range(steps):
+                fn()
+            e1.record()
+            torch.cuda.synchronize()
+            t.append(e0.elapsed_time(e1) / steps)
+        return statistics.median(t)
+    for what, batch, new, ctx, words in (("prompt", 1, 1024, 0, 0), ("decode", 64, 1, 2047, 0), ("drafts", 8, 32, 2048, 1)):
+        M, width = batch * new, -(-(new + ctx) // page)
+        st = AttentionStack(weights, M, batch, width, batch * width, page, words=words)
+        for src in (0, 4, 6):
+            st.set_input(0, src, torch.randn(st.x[0][src].shape, device=dev, generator=gen))
+        for c in (*st.k_cache, *st.v_cache):
+            c.normal_(generator=gen)
+        st.set_batch(torch.randperm(batch * width, device=dev, generator=gen).view(batch, width),
+                     torch.full((batch,), new + ctx, device=dev), torch.arange(batch + 1, device=dev) * new)
+        if words:                                 # node i below node i // 2 (0: the root)
+            bits, depth = [1], [0]
+            for i in range(1, new):
+                bits.append(bits[i // 2 if i > 1 else 0] | 1 << i)
+                depth.append(depth[i // 2 if i > 1 else 0] + 1)
+            st.set_tree(torch.tensor(bits * batch, dtype=torch.int64, device=dev).view(M, 1),
+                        torch.tensor([ctx + d for d in depth] * batch, dtype=torch.int32, device=dev))
+        graph, plain = st.capture("shared"), st.capture("gemm")
+        one = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(one):
+            st.attend(0)
+        ms, gemm_ms, us = timed(graph.replay), timed(plain.replay), timed(one.replay) * 1e3
+        print(json.dumps({"workload": f"{layers}-layer 7B-shaped stack with attention, {what}: {batch} x {new} tokens after {ctx}",
+                          "ms_per_pass": round(ms, 4), "ms_gemm_only": round(gemm_ms, 4), "attention_us_per_layer": round(us, 2),
+                          "data": "synthetic"}), flush=True)
+        del st, graph, plain, one
+
+
 def copy_calibration(nbytes: int, launches: int):
     import torch
     a = torch.empty(nbytes, dtype=torch.uint8, device="cuda:0").fill_(1)
@@ -560,6 +615,8 @@ def main():
                     help="time the 7B layer GEMM shapes over M = 16..2048 tokens: plain vs K-split entry points")
     ap.add_argument("--experts", action="store_true",
                     help="time the stack with MXFP4 experts for its FFN")
+    ap.add_argument("--attention", action="store_true",
+                    help="time the stack with attention over paged caches")
     ap.add_argument("--q6forms", action="store_true",
                     help="time the three q6_K weight forms on the v and down shapes over M = 16..1024")
     a = ap.parse_args()
@@ -576,6 +633,10 @@ def main():
     if a.experts:
         run_experts(a.steps if a.steps != ap.get_default("steps") else 20,
                     a.warmup if a.warmup != ap.get_default("warmup") else 3)
+        return
+    if a.attention:
+        run_attention(a.steps if a.steps != ap.get_default("steps") else 20,
+                      a.warmup if a.warmup != ap.get_default("warmup") else 3)
         return
     if a.shards or a.msweep or a.q6forms:
         if a.shards:

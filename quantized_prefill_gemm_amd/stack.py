@@ -212,3 +212,79 @@ class ExpertStack(Stack):
         """Of a pass whose choices all have an expert."""
         attention = self.M * sum(N * K for _, _, N, K in STACK_LAYER[:4])
         return self.L * (attention + self.S * sum(N * K for _, _, N, K in STACK_LAYER[4:]))
+
+
+class AttentionStack(Stack):
+    """The stack with the attention between its projections: in each layer the outputs of q, k and v go
+    through cache_append into that layer's paged cache, and the attention over the cache is o's input (the
+    stack's 4096 values are 32 heads of 128, keys and values of all 32). Prompts, tokens being decoded and both in one batch
+    are the same pass, and with `words` > 0 the new tokens are trees of drafts (set_tree).
+
+    M: rows of a pass, padding among them; B sequences of at most width pages of `page` tokens; the pool has `pages` pages for
+    each layer. set_batch gives the sequences, on the device: a captured pass replays with others.
+    Positions 0 and 4 (q/k/v's and gate/up's input) and 6 are given as in Stack.
+    """
+
+    HEADS, DIM = 32, 128
+
+    def __init__(self, weights, M: int, sequences: int, width: int, pages: int, page: int = 64, dtype=torch.float16,
+                 q6: str = "expanded", per_layer: bool = False, base: float = 10000.0, words: int = 0):
+        if not 1 <= sequences <= M:
+            raise ValueError(f"{sequences} sequences in {M} rows")
+        if width < 1 or pages < 1:
+            raise ValueError(f"tables of {width} pages, a pool of {pages}")
+        if words < 0:
+            raise ValueError(f"{words} words of tree")
+        super().__init__(weights, M, q6, per_layer)
+        dev, H, D = weights[0][0].device, self.HEADS, self.DIM
+        self.k_cache, self.v_cache = ([torch.zeros((pages, H, page, D), dtype=dtype, device=dev) for _ in range(self.L)]
+                                      for _ in range(2))
+        self.table = torch.zeros((sequences, width), dtype=torch.int32, device=dev)
+        self.lens = torch.zeros(sequences, dtype=torch.int32, device=dev)
+        self.offsets = torch.zeros(sequences + 1, dtype=torch.int32, device=dev)
+        self.tree = torch.zeros((M, words), dtype=torch.int64, device=dev) if words else None
+        self.positions = torch.zeros(M, dtype=torch.int32, device=dev) if words else None
+        at = torch.arange(0, D, 2, dtype=torch.float64)
+        self.freqs = (base ** (-at / D)).to(torch.float32).to(dev)
+        self.q = torch.empty((M, H, D), dtype=dtype, device=dev)
+        self.ws = torch.empty(max(B.cache_attention_bytes(M, sequences, H, H, D, width * page), 1), dtype=torch.uint8, device=dev)
+
+    def set_batch(self, table: torch.Tensor, lens: torch.Tensor, offsets: torch.Tensor):
+        """The sequences' pages, their lengths with the new tokens, and where their new rows begin."""
+        for to, t in ((self.table, table), (self.lens, lens), (self.offsets, offsets)):
+            to.copy_(t)
+
+    def set_tree(self, tree: torch.Tensor, positions: torch.Tensor):
+        """Of a stack with `words`: which nodes each new token sees, and its position."""
+        if self.tree is None:
+            raise ValueError("the stack was made without words for trees")
+        self.tree.copy_(tree)
+        self.positions.copy_(positions)
+
+    def attend(self, layer: int, stream=None):
+        """The layer's attention, from the outputs of q, k and v to o's input."""
+        io = self.io(layer)
+        kc, vc = self.k_cache[layer], self.v_cache[layer]
+        index = self.table, self.lens, self.offsets
+        B.cache_append(self.y[io][0], self.y[io][1], self.y[io][2], kc, vc, *index, freqs=self.freqs,
+                       positions=self.positions, adjacent=True, y=self.q, stream=stream)
+        y = self.x[io][3].view(self.M, self.HEADS, self.DIM)
+        if self.tree is None:
+            B.cache_attention(self.q, kc, vc, *index, y=y, ws=self.ws, stream=stream)
+        else:
+            B.cache_attention_tree(self.q, kc, vc, *index, self.tree, self.positions, y=y, ws=self.ws, stream=stream)
+
+    def run(self, mode: str = "shared", stream=None):
+        """As Stack.run, with the attention after a layer's v; `gemm` leaves it out, as it does the quantisation."""
+        if mode not in MODES:
+            raise ValueError(f"mode {mode!r}")
+        for layer in range(self.L):
+            io = self.io(layer)
+            for idx in range(len(STACK_LAYER)):
+                src = SOURCE[idx]
+                if idx == 3 and mode != "gemm":
+                    self.attend(layer, stream)
+                at = idx if mode == "all" else src
+                if mode == "all" or (mode == "shared" and src == idx):
+                    B.quantize_q8_1(self.x[io][src], self.xq[io][at], stream=stream)
+                self._gemm(layer, idx, self.xq[io][at], stream)
