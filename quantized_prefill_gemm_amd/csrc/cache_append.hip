@@ -56,7 +56,6 @@ __global__ void __launch_bounds__(256) cache_append_kernel(AppendArgs a)
     const int t = blockIdx.x, lanes = 1 << a.lane_bits;
     const int u = threadIdx.x & (lanes - 1), group = threadIdx.x >> a.lane_bits, groups = 256 >> a.lane_bits;
     const int first = blockIdx.y * a.per, all = a.heads + 2 * a.kv, end = min(first + a.per, all);
-    if (t < a.batch.offset(0) || t >= a.batch.offset(a.batch.B)) return;
     const bool on = 8 * u < a.dim;
 
     // where the lane's two fours are in a head, and whether they are rotated
@@ -83,10 +82,25 @@ __global__ void __launch_bounds__(256) cache_append_kernel(AppendArgs a)
     };
     load(first + group);           // under way while the place is looked up
 
-    const int b = last_not_above(a.batch.B, t, [&](int i) { return a.batch.offset(i); });
+    // The token's sequence, its numbers with those it is found by where there are few.
+    int b = 0, row0, row1, length;
+    if (a.batch.B < 64) {
+        const int lane = threadIdx.x & 63;
+        const int at = min(max(a.batch.offsets[min(lane, a.batch.B)], 0), a.batch.T), long_ = a.batch.lens[min(lane, a.batch.B - 1)];
+        const uint64_t hit = __ballot(lane < a.batch.B && at <= t);
+        b = hit ? 63 - __builtin_clzll(hit) : 0;
+        row0 = __builtin_amdgcn_readlane(at, b);
+        row1 = __builtin_amdgcn_readlane(at, b + 1);
+        length = __builtin_amdgcn_readlane(long_, b);
+    } else {
+        b = last_not_above(a.batch.B, t, [&](int i) { return a.batch.offset(i); });
+        row0 = a.batch.offset(b);
+        row1 = a.batch.offset(b + 1);
+        length = a.batch.lens[b];
+    }
+    if (t < row0 || t >= row1) return;                 // of no sequence
     const int64_t most = (int64_t)a.batch.width << a.page_bits;
-    const int64_t len = min((int64_t)max(a.batch.lens[b], 0), most);
-    const int64_t place = len - (a.batch.offset(b + 1) - t);
+    const int64_t place = min((int64_t)max(length, 0), most) - (row1 - t);
     int page = -1;
     if (place >= 0 && place < most) page = a.batch.table[(int64_t)b * a.batch.width + (place >> a.page_bits)];
     const bool kept = page >= 0 && page < a.pages;
