@@ -9,6 +9,10 @@
 // head is the lane's for all heads, so a lane has its four angles, and its eight weights, for the whole
 // token. Angles reach 1e6 and more, where f32 has no fraction left: the product with the
 // frequency is made in 64 bits, in turns, and its fraction goes to f32's sine and cosine.
+//
+// Bound by memory: 7622 tokens of 32 + 2 * 8 heads of 128, bf16, normed 39.9 us, 4.7 TB/s; 1024 tokens of 96 heads f32 to
+// f16 14.7 us, 5.1 TB/s. A few tokens are bound by the loads that find their place, one round behind the
+// other: one token 3.5 us. Weights read one by one instead of by four cost 49 us there, adjacent pairs 72.
 #include "qpg_cache.h"
 
 namespace qpg {
@@ -19,7 +23,7 @@ struct AppendArgs {
     int64_t q_stride, k_stride, v_stride;
     void *y, *kc, *vc;
     int64_t k_page, v_page;       // elements from page to page
-    int pages, page_bits, dim, heads, kv, rot, adjacent, lane_bits, per;
+    int pages, page_bits, dim, heads, kv, rot, lane_bits, per;
     const int32_t* positions;
     const float *freqs, *q_norm, *k_norm;
     float eps;
@@ -50,7 +54,29 @@ __device__ __forceinline__ void store4(T* p, const float (&f)[8], int at)
 
 constexpr int HEADS_AT_ONCE = 3;   // a lane's loads of so many heads are under way together
 
-template <typename TI, typename TC, bool VEC>
+// The sum over aligned groups of 2^bits lanes, in all of them. A step's partner holds the other half's sum whichever of
+// its lanes it is, so mirrors do for exchanges.
+__device__ __forceinline__ float group_sum(float x, int bits)
+{
+    auto with = [](float v, auto how) {
+        return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(how)::value, 0xF, 0xF, false));
+    };
+    if (bits > 0) x = with(x, std::integral_constant<int, 0xB1>());        // lane ^ 1
+    if (bits > 1) x = with(x, std::integral_constant<int, 0x4E>());        // lane ^ 2
+    if (bits > 2) x = with(x, std::integral_constant<int, 0x141>());       // mirrored in eight lanes
+    if (bits > 3) x = with(x, std::integral_constant<int, 0x140>());       // mirrored in sixteen
+    if (bits > 4) x += __shfl_xor(x, 16);
+    return x;
+}
+
+// 1 / sqrt(x), to a step; x is scaled to where the instruction takes it (it has no subnormal numbers).
+__device__ __forceinline__ float inverse_root(float x)
+{
+    const bool tiny = x < 0x1p-100f;
+    return __builtin_amdgcn_rsqf(tiny ? x * 0x1p80f : x) * (tiny ? 0x1p40f : 1.0f);
+}
+
+template <typename TI, typename TC, bool VEC, bool ADJACENT, bool NORM>
 __global__ void __launch_bounds__(256) cache_append_kernel(AppendArgs a)
 {
     const int t = blockIdx.x, lanes = 1 << a.lane_bits;
@@ -59,7 +85,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(AppendArgs a)
     const bool on = 8 * u < a.dim;
 
     // where the lane's two fours are in a head, and whether they are rotated
-    const bool turn = 8 * u < a.rot, split = turn && !a.adjacent;
+    const bool turn = 8 * u < a.rot, split = turn && !ADJACENT;
     const int o0 = split ? 4 * u : 8 * u, o1 = split ? 4 * u + a.rot / 2 : 8 * u + 4;
     const TI* q = static_cast<const TI*>(a.q) + t * a.q_stride;
     const TI* k = static_cast<const TI*>(a.k) + t * a.k_stride;
@@ -118,12 +144,19 @@ __global__ void __launch_bounds__(256) cache_append_kernel(AppendArgs a)
             sincospif((float)(2.0 * turns), &s[i], &c[i]);
         }
     }
+    if (NORM) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int d = i < 4 ? o0 + i : o1 + i - 4;
-        wq[i] = on && a.q_norm ? a.q_norm[d] : 1.0f;
-        wk[i] = on && a.k_norm ? a.k_norm[d] : 1.0f;
+        for (int i = 0; i < 8; ++i) wq[i] = wk[i] = 1.0f;
+        if (on && a.q_norm) {
+            load4<VEC>(a.q_norm + o0, wq, 0);
+            load4<VEC>(a.q_norm + o1, wq, 4);
+        }
+        if (on && a.k_norm) {
+            load4<VEC>(a.k_norm + o0, wk, 0);
+            load4<VEC>(a.k_norm + o1, wk, 4);
+        }
     }
+    const float share = 1.0f / (float)a.dim;
 
     for (int h0 = first + group; h0 < end; h0 += HEADS_AT_ONCE * groups) {
 #pragma unroll
@@ -131,21 +164,23 @@ __global__ void __launch_bounds__(256) cache_append_kernel(AppendArgs a)
             const int h = h0 + i * groups;
             const bool is_q = h < a.heads, is_k = !is_q && h < a.heads + a.kv;
             float (&f)[8] = x[i];
-            if ((is_q && a.q_norm) || (is_k && a.k_norm)) {
+            if (NORM) {                                // by all lanes: the sum's exchanges are of whole groups
                 float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum += f[j] * f[j];
-                for (int m = lanes >> 1; m; m >>= 1) sum += __shfl_xor(sum, m);
-                const float r = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
+                const float r = inverse_root(group_sum(sum, a.lane_bits) * share + a.eps);
+                if ((is_q && a.q_norm) || (is_k && a.k_norm)) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] *= r * (is_q ? wq[j] : wk[j]);
+                    for (int j = 0; j < 8; ++j) f[j] *= r * (is_q ? wq[j] : wk[j]);
+                }
             }
             if (turn && (is_q || is_k)) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float p = a.adjacent ? f[2 * j] : f[j], r = a.adjacent ? f[2 * j + 1] : f[j + 4];
-                    const float p1 = p * c[j] - r * s[j], r1 = p * s[j] + r * c[j];
-                    if (a.adjacent) { f[2 * j] = p1; f[2 * j + 1] = r1; } else { f[j] = p1; f[j + 4] = r1; }
+                    float &p = f[ADJACENT ? 2 * j : j], &q2 = f[ADJACENT ? 2 * j + 1 : j + 4];
+                    const float p1 = p * c[j] - q2 * s[j], q1 = p * s[j] + q2 * c[j];
+                    p = p1;
+                    q2 = q1;
                 }
             }
             if (!on || h >= end || (!is_q && !kept)) continue;
@@ -180,21 +215,29 @@ hipError_t qpg_launch_cache_append(const qpg_cache& cache, const qpg_batch& batc
     auto fits = [&](const void* p, int64_t stride) {
         return (uintptr_t)p % unit == 0 && (size_t)stride * type_bytes(type) % unit == 0;
     };
-    const bool vec = (!heads || fits(q, q_stride)) && fits(k, k_stride) && fits(v, v_stride);
+    // accesses of four values, the weights' among them: else one by one
+    const bool vec = (!heads || fits(q, q_stride)) && fits(k, k_stride) && fits(v, v_stride) && (uintptr_t)q_norm % 16 == 0 &&
+                     (uintptr_t)k_norm % 16 == 0;
     const AppendArgs a = {{batch.table, batch.lens, batch.offsets, (int)batch.B, (int)batch.width, (int)batch.T},
                           q, k, v, q_stride, k_stride, v_stride, y, cache.k, cache.v, cache.k_stride, cache.v_stride,
-                          (int)cache.pages, page_bits, (int)cache.dim, (int)heads, (int)cache.heads, (int)rot, adjacent,
+                          (int)cache.pages, page_bits, (int)cache.dim, (int)heads, (int)cache.heads, (int)rot,
                           lane_bits, (int)per, positions, freqs, q_norm, k_norm, eps};
     const dim3 grid((unsigned)batch.T, (unsigned)((all + per - 1) / per));
     return qpg_by_type(type, [&](auto ti) {
         typedef typename Store<decltype(ti)::value>::type TI;
         auto run = [&](auto tc) {
             typedef typename Store<decltype(tc)::value>::type TC;
-            if (vec)
-                hipLaunchKernelGGL((cache_append_kernel<TI, TC, true>), grid, dim3(256), 0, s, a);
-            else
-                hipLaunchKernelGGL((cache_append_kernel<TI, TC, false>), grid, dim3(256), 0, s, a);
-            return hipGetLastError();
+            auto go = [&](auto adj, auto norm) {
+                constexpr bool A = decltype(adj)::value, N = decltype(norm)::value;
+                if (vec)
+                    hipLaunchKernelGGL((cache_append_kernel<TI, TC, true, A, N>), grid, dim3(256), 0, s, a);
+                else
+                    hipLaunchKernelGGL((cache_append_kernel<TI, TC, false, A, N>), grid, dim3(256), 0, s, a);
+                return hipGetLastError();
+            };
+            const bool norm = q_norm || k_norm;
+            if (adjacent) return norm ? go(std::true_type(), std::true_type()) : go(std::true_type(), std::false_type());
+            return norm ? go(std::false_type(), std::true_type()) : go(std::false_type(), std::false_type());
         };
         return cache.type == QPG_F16 ? run(std::integral_constant<int, QPG_F16>()) : run(std::integral_constant<int, QPG_BF16>());
     });

@@ -16,7 +16,8 @@ def freqs_of(rot, base=10000.0):
     return (base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)).float()
 
 
-def run(batch, heads, x="f32", rot=0, adjacent=False, norm=False, positions=None, fused=False, shift=0, eps=1e-6, base=10000.0):
+def run(batch, heads, x="f32", rot=0, adjacent=False, norm=False, positions=None, fused=False, shift=0, eps=1e-6, base=10000.0,
+        weights_at=0):
     wide = [heads * batch.dim, batch.kv * batch.dim, batch.kv * batch.dim]
     q, k, v = (batch.normal(batch.rows, w, scale=2.0, kind=x) if w else None for w in wide)
     kw = {"adjacent": adjacent, "eps": eps, "freqs": freqs_of(rot, base) if rot else None,
@@ -37,6 +38,9 @@ def run(batch, heads, x="f32", rot=0, adjacent=False, norm=False, positions=None
     kc, vc = (t.to(DEV) for t in before)
     y = torch.full((batch.rows, heads, batch.dim), 777.0, dtype=batch.dtype, device=DEV) if heads else None
     kw = {n: t.to(DEV) if isinstance(t, torch.Tensor) else t for n, t in kw.items()}
+    for n in ("q_norm", "k_norm"):                      # at any element of a buffer
+        if kw[n] is not None:
+            kw[n] = torch.cat([torch.zeros(weights_at, device=DEV), kw[n]])[weights_at:]
     got = qpg.cache_append(dq, dk, dv, kc, vc, *batch.index(DEV), y=y, **kw)
     torch.cuda.synchronize()
     lead, end = int(batch.offsets[0]), int(batch.offsets[-1])
@@ -83,6 +87,11 @@ def test_head_layouts(heads, kv, page):
 def test_slices_of_one_product(shift, x):
     """Rows at any distance, and beginning at any element."""
     run(R.Batch([2, 5], [30, 5], 3, 40, 16, "bf16", seed=shift), 6, x, 40, False, True, fused=True, shift=shift)
+
+
+@pytest.mark.parametrize("weights_at", [1, 2, 3])
+def test_norm_weights_at_any_element(weights_at):
+    run(R.Batch([2, 5], [30, 5], 3, 40, 16, "bf16", seed=3), 6, "f32", 40, True, True, weights_at=weights_at)
 
 
 def test_tokens_by_the_thousand():
