@@ -51,6 +51,10 @@ int attention(const qpg_cache* cache, const qpg_batch* batch, const qpg_scores* 
     if (!(scores->scale > 0.0f) || !isfinite(scores->scale) || !(scores->cap >= 0.0f) || !isfinite(scores->cap) ||
         scores->window < 0)
         return QPG_EINVAL;
+    // the kernel's factors, in powers of two
+    if (!isfinite(1.5f * scores->scale) || !isfinite(1.5f * scores->cap) ||
+        (scores->cap > 0.0f && !isfinite(3.0f * scores->scale / scores->cap)))
+        return QPG_EINVAL;
     if (qpg_cache_attention_grid(batch->T, batch->B, heads, cache->heads, cache->dim, batch->width * cache->page) >= kMaxRows)
         return QPG_EINVAL;
     if (!ws && qpg_cache_attention_bytes(batch->T, batch->B, heads, cache->heads, cache->dim, batch->width * cache->page))

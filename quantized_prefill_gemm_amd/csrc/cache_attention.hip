@@ -122,14 +122,14 @@ constexpr int NO_WINDOW = 1 << 30;
 constexpr float LOG2E = 1.4426950408889634f;
 
 // cap tanh(x) = cap - 2 cap / (exp(2x) + 1), with `cap` in powers of two and exp(2x) = 2^(s * cap_scale). Next to 0, where
-// that cancels, FINE takes the series to x^9 (the next term is below 2^-24 of x up to |x| = 0.2); without it the
-// error is a few steps of 1 times the cap, far below a share's rounding to 16 bits.
-template <bool FINE>
-__device__ __forceinline__ float capped(float s, float cap, float cap_scale)
+// that cancels, `fine` takes the series to x^9 (the next term is below 2^-24 of x up to |x| = 0.2); without it the
+// error is a few steps of 1 times the cap: up to COARSE_CAP far below a share's rounding to 16 bits.
+constexpr float COARSE_CAP = 128.0f * LOG2E;
+__device__ __forceinline__ float capped(float s, float cap, float cap_scale, bool fine)
 {
     const float t = s * cap_scale;
     const float big = cap - 2.0f * cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(t) + 1.0f);
-    if (!FINE) return big;
+    if (!fine) return big;
     const float z = t * 0.34657359027997264f, z2 = z * z;               // ln(2) / 2
     const float small = cap * (z + z * z2 * (-0.33333333333f + z2 * (0.13333333333f + z2 * (-0.053968253968f + z2 * 0.021869488536f))));
     return fabsf(z) < 0.2f ? small : big;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     const int begin_stage = max(begin / KT, head_stages), end_stage = (end + KT - 1) / KT;
     const int stages = head_stages + max(end_stage - begin_stage, 0);
     auto key_of = [&](int i) { return (i < head_stages ? i : i - head_stages + begin_stage) * KT; };
-    const int share = max((divide(stages + a.splits - 1, a.splits) + WK - 1) / WK * WK, WK * a.least);
+    const int share = max(((stages + a.splits - 1) / a.splits + WK - 1) / WK * WK, WK * a.least);
     const int i0 = min(split * share, stages), i1 = min(i0 + share, stages);
     const bool parts = stages > share;                 // else the first piece is all, and writes y
     if (!parts && split > 0) return;
@@ -416,10 +416,17 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         if (key < plain_low || last > plain_high) {
             if (a.cap > 0.0f) {
                 c = 1.0f;
+                if (NP > 1 || a.cap > COARSE_CAP) {
 #pragma unroll
-                for (int e = 0; e < NS; ++e)
+                    for (int e = 0; e < NS; ++e)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[e][r] = capped<(NP > 1)>(s[e][r], a.cap, a.cap_scale);
+                        for (int r = 0; r < 16; ++r) s[e][r] = capped(s[e][r], a.cap, a.cap_scale, true);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < NS; ++e)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) s[e][r] = capped(s[e][r], a.cap, a.cap_scale, false);
+                }
             }
             const bool whole = a.tree ? last < ctx && (a.window >= NO_WINDOW || high - key < a.window)
                                       : last < n && (last < prefix || (last <= wave_low && wave_high - key < a.window));
@@ -556,7 +563,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
                         for (int e = 0; e < 8; ++e) x += (float)kv[e] * (float)qt[t][e];
                     }
                 x = half_sum(x);
-                x = a.cap > 0.0f ? capped<true>(x, a.cap, a.cap_scale) : x * a.scale;
+                x = a.cap > 0.0f ? capped(x, a.cap, a.cap_scale, true) : x * a.scale;
                 const int at = key_position(j);
                 if (a.slopes) x -= slope * fabsf((float)(position - at));
                 if (!(seen_from(j) & 1) || (a.tree && at < from)) continue;

@@ -129,8 +129,8 @@ def attention(batch, q, y_type, scale=None, cap=0.0, slopes=None, window=0, pref
             off = (dim + 8) * STEP * size
             if cap:
                 s = cap * torch.tanh(s / cap)
-                # 1 - 2 / (e + 1): a few steps of 1, times the cap; with a finer output of the value itself
-                off = off + (16 * STEP * cap if u == half(batch.dtype) else 16 * STEP * s.abs())
+                # 1 - 2 / (e + 1): a few steps of 1, times the cap; with a finer output or a large cap of the value itself
+                off = off + (16 * STEP * cap if u == half(batch.dtype) and cap <= 128 else 16 * STEP * s.abs())
             if slopes is not None:
                 bias = float(slopes[h]) * far.abs().to(F64)
                 s = s - bias

@@ -39,7 +39,8 @@ BAD_BATCH = [({"table": 0}, EINVAL), ({"lens": 0}, EINVAL), ({"offsets": 0}, EIN
              ({"width": 0}, EINVAL), ({"width": 2 ** 26 + 1}, EINVAL), ({"T": 0}, EINVAL), ({"T": 2 ** 24}, EINVAL),
              ({"table": A + 2}, EALIGN), ({"lens": A + 1}, EALIGN), ({"offsets": A + 2}, EALIGN)]
 BAD_SCORES = [({"scale": 0.0}, EINVAL), ({"scale": -1.0}, EINVAL), ({"scale": math.nan}, EINVAL), ({"scale": math.inf}, EINVAL),
-              ({"cap": -1.0}, EINVAL), ({"cap": math.nan}, EINVAL), ({"cap": math.inf}, EINVAL), ({"window": -1}, EINVAL),
+              ({"cap": -1.0}, EINVAL), ({"cap": math.nan}, EINVAL), ({"cap": math.inf}, EINVAL), ({"scale": 3e38}, EINVAL), ({"cap": 3e38}, EINVAL), ({"cap": 1e-39}, EINVAL),
+              ({"scale": 1e20, "cap": 1e-20}, EINVAL), ({"window": -1}, EINVAL),
               ({"slopes": A + 2}, EALIGN)]
 
 

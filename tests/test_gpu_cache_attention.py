@@ -115,7 +115,7 @@ def test_prefixes(prefix, window):
 
 
 @pytest.mark.parametrize("y", ["f32", "f16"])
-@pytest.mark.parametrize("cap", [0.5, 3.0, 50.0, 1e6])
+@pytest.mark.parametrize("cap", [0.5, 3.0, 50.0, 128.0, 129.0, 1e6])
 def test_caps(cap, y):
     run(R.Batch([70, 1], [100, 33], 2, 80, 16, "f16", seed=3), 2, y, cap=cap, q_scale=8.0)
 
@@ -329,3 +329,27 @@ def test_forms(case, kind, y):
             want, bound, _ = R.attention(one, q[at:at + n, h:h + 1], y)
             check(got[at:at + n, h:h + 1], want, bound)
         at += n
+
+
+def test_the_longest_sequence():
+    """2^29 tokens and a few: the pieces cover all of them. Keys are alike but for some, so the shares are known."""
+    page, dim = 256, 8
+    length = (1 << 29) + 300
+    pages = -(-length // page)
+    k = torch.zeros((pages, 1, page, dim), dtype=torch.float16, device=DEV)
+    v = torch.zeros((pages, 1, page, dim), dtype=torch.float16, device=DEV)
+    rows = k.view(-1, dim)
+    at = torch.tensor([0, 1 << 20, (1 << 24) + 7, (1 << 28) + 5, (1 << 29) - 1, 1 << 29, length - 1], device=DEV)
+    rows[:, 0] = -30.0                                 # shares of e^-60 of the others': together 2^29 e^-60, below 2^-50
+    rows[at, 0] = 30.0
+    v.view(-1, dim)[at, 1] = torch.arange(1, len(at) + 1, dtype=torch.float16, device=DEV)
+    q = torch.zeros((1, 1, dim), dtype=torch.float16, device=DEV)
+    q[0, 0, 0] = 1.0
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, -1)
+    lens, offsets = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([length], [0, 1]))
+    for window in (0, 1 << 28, length - 1):
+        seen = int((length - 1 - at < (window or length)).sum())
+        y = qpg.cache_attention(q, k, v, table, lens, offsets, scale=1.0, window=window, dtype=torch.float32)[0, 0].cpu().double()
+        values = torch.arange(len(at) - seen + 1, len(at) + 1, dtype=torch.float64)
+        # shares are powers of exactly equal scores: equal; sums of a few terms
+        assert abs(float(y[1]) - float(values.mean())) <= 64 * 2.0 ** -24 * 7 and float(y[0]) == 0 and bool((y[2:] == 0).all())
