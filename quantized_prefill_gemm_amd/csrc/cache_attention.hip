@@ -22,7 +22,7 @@
 // 8192 tokens of 32 query over 8 heads of 128 in bf16 525 us, 1.05 PFLOP/s, the matrix units busy 54 % of the time and
 // the vector units 48 % (powers are a quarter of a step's vector cycles), no LDS conflicts. (A pipeline of 32-key steps, one's K Q^T
 // among the powers of the one before, came to 557 to 619.) Decoding is bound by memory: 64 tokens over 130 to
-// 8100 of 8 heads 193 us, 5.4 TB/s. Few tiles are bound by the time of a tile's rounds, about 1.1 us each and 2.6
+// 8100 of 8 heads 190 us, 5.5 TB/s. Few tiles are bound by the time of a tile's rounds, about 1.1 us each and 2.6
 // where eight waves share a CU, and of 7 us around them: finding the tile, the first loads, the join. What that time
 // was before: a table read by vector loads, whose wait was one for the prefetch as well, made the decode batch 251.
 #include "qpg_cache.h"
@@ -735,17 +735,17 @@ struct AttentionForm {
 
 // Chosen by what the host knows: the mean number of columns and the longest length that the table holds. Both sides
 // measured (us, heads of 128 unless said; MHA: 32 of 32 heads, GQA: 32 of 8):
-//   tiles of 128 where they are 256 and more, shared by two groups of waves up to 1024 of them: prompts of 1024 to
-//     4096 tokens MHA 35, 72, 172 against 43, 74, 185 by one group; of 8192 GQA, 2048 tiles, 581 against 542
-//   else tiles of 64 where they are 192 and more (512 tokens MHA 16.0; tiles of 128 19.5, of 32 22.4), and of 32 below
-//     (256 tokens 11.0; of 64 12.9; 26 drafts over 2048 tokens GQA 18.0; of 64 21.1, of 128 22.4)
-//   but not over long caches, where larger tiles in pieces read less: 512 tokens over 8000 GQA 87 against 104 of 64
-//     and 146 of 32; 128 tokens over 8000 39.6 (64, four pieces) against 47.9 (32)
-//   heads of up to 256: tiles of 128 from 512 of them (4096 tokens, 16 of 8 heads: 229, of 64 252; 1024 tokens: of
-//     64 39.7, of 128 51.5)
-//   pieces until there are about 128 workgroups, since joining them costs 4 us and more (one token over 4096, MHA: one
-//     piece 32, four 23.0, eight 23.8), and two where long caches would leave CUs without work at the end
-//     (64 tokens over up to 8100 GQA: 230, 197 with two). A piece has at least 256 keys.
+//   tiles of 128 where they are 256 and more, shared by two groups of waves up to 1024 of them: prompts of 1024, 2048,
+//     4096 tokens MHA 34, 69, 176 against 41, 71, 175 by one group; of 8192 GQA, 2048 tiles, 570 against 523
+//   else tiles of 64 where they are 192 and more (512 tokens MHA 15.9; tiles of 128 19.6, of 32 22.6), and of 32 below
+//     (256 tokens 11.1; of 64 12.9; 26 drafts over 2048 tokens GQA 16.6; of 64 19.2, of 128 20.1)
+//   but not over long caches, where larger tiles in pieces read less: 512 tokens over 8000 GQA 87 against 98 of 64
+//     and 152 of 32; 128 tokens over 8000 37.8 (64, four pieces) against 48.3 (32)
+//   heads of up to 256: tiles of 128 from 512 of them (4096 tokens, 16 of 8 heads: 204, of 64 250; 1024 tokens: of
+//     64 38.8, of 128 48.9)
+//   pieces until there are about 128 workgroups, since joining them costs 3 us and more (one token over 4096, MHA: one
+//     piece 41, two 28.6, four 21.4, eight 22.2), and four where long caches would leave CUs without work at the end
+//     (64 tokens over up to 8100 GQA: one piece 203, two 196, four 190, eight 219). A piece has at least 256 keys.
 AttentionForm form_of(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length)
 {
     const int64_t group = heads / kv, busy = B < T ? B : T, mean = (T * group + busy - 1) / busy;
@@ -767,7 +767,7 @@ AttentionForm form_of(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t d
     }
     const int64_t count = tiles(32 * f.wc), goal = f.wc == 1 ? 128 : 256;
     int64_t splits = (goal + count - 1) / count;
-    if (splits < 2 && far && f.wc == 1 && count <= 1024) splits = 2;
+    if (splits < 4 && far && f.wc == 1 && count <= 1024) splits = 4;
     if (f.wc > 1 && !far) splits = 1;
     if (splits > length / 256) splits = length / 256;
     if (splits > 64) splits = 64;

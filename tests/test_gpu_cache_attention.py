@@ -353,3 +353,32 @@ def test_the_longest_sequence():
         values = torch.arange(len(at) - seen + 1, len(at) + 1, dtype=torch.float64)
         # shares are powers of exactly equal scores: equal; sums of a few terms
         assert abs(float(y[1]) - float(values.mean())) <= 64 * 2.0 ** -24 * 7 and float(y[0]) == 0 and bool((y[2:] == 0).all())
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed in turn on one stream, with eager work between: each call writes all of the workspace that it reads."""
+    made = []
+    batches = [R.Batch([1, 1], [5000, 900], 2, 128, 64, "bf16", seed=1), R.Batch([30], [3000], 1, 64, 64, "bf16", seed=2)]
+    sizes = [qpg.cache_attention_bytes(2, 2, 8, 2, 128, batches[0].width * 64), qpg.cache_attention_bytes(30, 1, 4, 1, 64, batches[1].width * 64)]
+    assert min(sizes) > 0
+    ws = torch.full((max(sizes),), 255, dtype=torch.uint8, device=DEV)
+    for b, heads in zip(batches, (8, 4)):
+        args = (b.normal(b.rows, heads, b.dim).to(DEV), b.k.to(DEV), b.v.to(DEV), *b.index(DEV))
+        want = qpg.cache_attention(*args)
+        y = torch.zeros_like(want)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            qpg.cache_attention(*args, y=y, ws=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            qpg.cache_attention(*args, y=y, ws=ws)
+        made.append((graph, args, y, want))
+    for turn in (0, 1, 1, 0, 1, 0):
+        graph, args, y, want = made[turn]
+        y.zero_()
+        graph.replay()
+        again = qpg.cache_attention(*args)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(again, want)
