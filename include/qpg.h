@@ -25,8 +25,8 @@
  *     and the device are checked before anything is enqueued, so on QPG_EINVAL,
  *     QPG_EALIGN and QPG_EDEVICE nothing has been. QPG_EHIP reports a failed kernel
  *     launch; in the entry points that enqueue two kernels (mmq_q4K / mmq_q6K: quantise,
- *     then the MMQ; the _sk entry points with a split: the MMQ, then the reduce; mmq_mxfp4, experts_sort
- *     and the _zero entry points likewise) the first may already be enqueued when the second fails.
+ *     then the MMQ; the _sk entry points with a split: the MMQ, then the reduce; mmq_mxfp4, experts_sort,
+ *     the _zero entry points and the attentions over a cache likewise) the first may already be enqueued when the second fails.
  *     QPG_ESCRATCH (mmq_q4K_noalloc only) is reported before anything is enqueued. There is no
  *     fallback path.
  *   - The library runs on gfx950 only (QPG_EDEVICE otherwise).
@@ -384,7 +384,8 @@ typedef struct qpg_scores {
  *   the cache. Key j's position is j. Keys and values that a row does not see do not touch it, whatever they hold.
  *   Scores and sums are f32. The shares that multiply the values are rounded to the cache's type (half a
  *   step each); with a y_type of more bits than that they are two (f16) or three (bf16) pieces, which
- *   leave f32's own errors (and make NaN of an infinite value that a row sees).
+ *   leave f32's own errors. A row that sees an infinite value is infinite or, where a piece of its share is 0 or less,
+ *   NaN.
  * cache_attention_tree: the new tokens of a sequence are nodes of a tree of drafts. A node sees the tokens before the
  *   new ones, and node m iff bit m % 64 of word m / 64 of its row of `tree` (int64 [T][words]) is set: its ancestors and itself.
  *   positions int32 [T], 0 .. 2^30, are the nodes' (the length before plus the depth), for window and slopes;

@@ -13,8 +13,9 @@ DEV = "cuda"
 
 
 def run(batch, heads, y="same", scale=None, cap=0.0, bias=False, window=0, prefix=None, tree=0, q_scale=1.0, give=True,
-        change=None):
-    """The call and its check. tree: branches of random trees; change: edits (batch, q) before the call, and what it sees."""
+        change=None, small=False):
+    """The call and its check. tree: branches of random trees; change: edits (batch, q) before the call, and what it sees;
+    small: shares may be too small for the cache's type."""
     y = batch.kind if y == "same" else y
     q = batch.normal(batch.rows, heads, batch.dim, scale=q_scale)
     kw = {"cap": cap, "window": window}
@@ -45,14 +46,15 @@ def run(batch, heads, y="same", scale=None, cap=0.0, bias=False, window=0, prefi
     torch.cuda.synchronize()
     assert got.shape == q.shape and got.dtype == R.TYPES[y]
     got = got.cpu().double()
-    check(got[mine], want[mine], bound[mine], pieces=R.half(R.TYPES[y]) < R.half(batch.dtype))
+    check(got[mine], want[mine], bound[mine], pieces=small or R.half(R.TYPES[y]) < R.half(batch.dtype))
     if give:
         assert bool((got[~mine] == float(torch.tensor(777.0).to(R.TYPES[y]))).all())
     return got, want, mine
 
 
 def check(got, want, bound, pieces=False):
-    """pieces: shares in several pieces, some of which may be 0 or below: with an infinite value they make NaN."""
+    """pieces: shares in several pieces, some of which may be 0 or below, or shares that may round to 0: with an infinite
+    value they make NaN."""
     assert torch.equal(torch.isfinite(got), torch.isfinite(want))
     odd = torch.isinf(want) & ~(torch.isnan(got) if pieces else torch.zeros_like(got, dtype=torch.bool))
     assert torch.equal(got[odd], want[odd])
@@ -382,3 +384,41 @@ def test_two_graphs_share_a_workspace():
         again = qpg.cache_attention(*args)
         torch.cuda.synchronize()
         assert torch.equal(y, want) and torch.equal(again, want)
+
+
+def draw(seed):
+    """A random call: sequences, heads, masks and all; values that are no numbers in one of four."""
+    import random
+    r = random.Random(seed)
+    kind = r.choice(["f16", "bf16"])
+    kv = r.choice([1, 1, 2, 3, 8])
+    group = r.choice([1, 1, 2, 3, 4, 7, 8])
+    dim = 8 * r.choice([1, 2, 5, 8, 8, 10, 12, 16, 16, 17, 24, 32])
+    tree = r.choice([0, 0, 1, 3])
+    B = r.choice([1, 2, 3, 5, 66])
+    most = 3 if B > 5 else r.choice([1, 2, 9, 40, 150])
+    new = [r.randint(0, most) for _ in range(B)]
+    new[r.randrange(B)] = most
+    far = r.choice([0, 5, 70, 300] if B > 5 else [0, 5, 70, 700, 2500])
+    lens = [max(0, n + r.randint(0, far) - (r.choice([0, 0, 0, 4]) if not tree else 0)) for n in new]
+    batch = R.Batch(new, lens, kv, dim, r.choice([16, 32, 64, 128, 256]), kind, seed=seed, lead=r.choice([0, 0, 2]), pad=r.choice([0, 0, 3]),
+                    extra_width=r.choice([0, 0, 1, 40]))
+    kw = {"y": r.choice(["same", "f32", "f16", "bf16"]), "cap": r.choice([0.0, 0.0, 5.0, 40.0, 1000.0]), "bias": r.random() < 0.3,
+          "window": r.choice([0, 0, 1, 17, 64, 300]), "tree": tree, "q_scale": r.choice([0.3, 1.0, 4.0]), "small": True}
+    if not tree and r.random() < 0.3:
+        kw["prefix"] = [r.randint(0, 400) for _ in range(B)]
+    if r.random() < 0.25:
+        def change(b, q):
+            for _ in range(3):
+                s = r.randrange(B)
+                if lens[s]:
+                    j = r.randrange(lens[s])
+                    b.v[b.table[s, j // b.page], :, j % b.page, r.randrange(dim)] = r.choice([math.nan, math.inf, -math.inf])
+        kw["change"] = change
+    return batch, kv * group, kw
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_calls(seed):
+    batch, heads, kw = draw(seed)
+    run(batch, heads, **kw)
