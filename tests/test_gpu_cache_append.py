@@ -48,7 +48,8 @@ def run(batch, heads, x="f32", rot=0, adjacent=False, norm=False, positions=None
         assert got is y
         got = got.cpu().double()
         assert float(((got - wq).abs() - bq)[lead:end].max()) <= 0, float(((got - wq).abs() / bq)[lead:end].max())
-        assert bool((got[:lead] == 777.0).all()) and bool((got[end:] == 777.0).all())
+        left = float(torch.tensor(777.0).to(batch.dtype))
+        assert bool((got[:lead] == left).all()) and bool((got[end:] == left).all())
     else:
         assert got is None
     for c, old, want, bound in ((kc, before[0], wk, bk), (vc, before[1], wv, bv)):
@@ -198,3 +199,28 @@ def test_graph_replays_and_streams():
         assert float(((results[0][2].cpu().double() - wq).abs() - bq)[:n].max()) <= 0 and bool((results[0][2][n:] == 9.0).all())
         for row, page, place in where:
             assert float(((results[0][0][page, :, place].cpu().double() - wk[row]).abs() - bk[row]).max()) <= 0
+
+
+def draw(seed):
+    """A random call: sequences, heads, types, rotated part, slices."""
+    import random
+    r = random.Random(seed)
+    dim = 8 * r.choice([1, 2, 5, 8, 8, 10, 16, 16, 17, 24, 32])
+    kv, B = r.choice([1, 2, 3, 8]), r.choice([1, 2, 3, 70])
+    new = [r.randint(0, r.choice([1, 3, 60] if B < 5 else [1, 2])) for _ in range(B)]
+    new[r.randrange(B)] += 1
+    lens = [max(0, n + r.randint(0, 200) - r.choice([0, 0, 0, 3])) for n in new]
+    batch = R.Batch(new, lens, kv, dim, r.choice([16, 32, 64, 128, 256]), r.choice(["f16", "bf16"]), seed=seed, lead=r.choice([0, 2]),
+                    pad=r.choice([0, 3]), extra_width=r.choice([0, 2]))
+    kw = {"x": r.choice(["f32", "f16", "bf16"]), "rot": r.choice([0, dim, 8 * r.randint(0, dim // 8)]), "adjacent": r.random() < 0.5,
+          "norm": r.random() < 0.5, "fused": r.random() < 0.5, "shift": r.choice([0, 0, 8, 3]), "eps": r.choice([1e-6, 1e-5, 0.0]),
+          "weights_at": r.choice([0, 0, 1])}
+    if r.random() < 0.3:
+        kw["positions"] = [r.randint(0, 200000) for _ in range(batch.rows)]
+    return batch, kv * r.choice([0, 1, 2, 3, 7]), kw
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_random_calls(seed):
+    batch, heads, kw = draw(seed)
+    run(batch, heads, **kw)
