@@ -387,7 +387,8 @@ typedef struct qpg_scores {
  *   leave f32's own errors. A row that sees an infinite value is infinite or, where a piece of its share is 0 or less,
  *   NaN.
  * cache_attention_tree: the new tokens of a sequence are nodes of a tree of drafts. A node sees the tokens before the
- *   new ones, and node m iff bit m % 64 of word m / 64 of its row of `tree` (int64 [T][words]) is set: its ancestors and itself.
+ *   new ones, and node m iff bit m % 64 of word m / 64 of its row of `tree` (int64 [T][words]) is set: its ancestors and itself,
+ *   in any order of the nodes.
  *   positions int32 [T], 0 .. 2^30, are the nodes' (the length before plus the depth), for window and slopes;
  *   nodes from 64 * words on are seen by none. 1 <= words <= 1024. prefix must be null.
  *   ws: qpg_cache_attention_bytes(T, B, heads, cache heads, dim, width * page) bytes, 16-byte aligned

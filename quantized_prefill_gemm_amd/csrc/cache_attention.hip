@@ -253,7 +253,9 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         wave_high = ctx + __builtin_amdgcn_readfirstlane(token_of(min(32 * wc + 31, columns - 1)));
     }
     // Positions are at most 2^30 and windows are clamped to it: no difference here overflows.
-    const int begin = a.window < NO_WINDOW ? max(low - a.window + 1, 0) : 0;
+    // The window bounds the places of earlier tokens alone, whose positions they are: a node may lie before its ancestors.
+    int begin = a.window < NO_WINDOW ? max(low - a.window + 1, 0) : 0;
+    if (a.tree) begin = min(begin, max(ctx, 0));
     const int end = a.tree ? n : min(n, max(high + 1, prefix));
     // Stages: those of the prefix, then those from the window on.
     const int head_stages = (min(prefix, end) + KT - 1) / KT;
