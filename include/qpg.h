@@ -339,7 +339,9 @@ int experts_combine_grad_zero(const void* dy, int dy_type, const void* ys, int y
  *     [0, T], lens to [0, width * page], entries of the table to [0, pages). An entry that no visible key needs may
  *     hold anything.
  *   1 <= B <= 2^20, 1 <= T < 2^24, 1 <= heads <= 4096, query heads a multiple of the cache's, T * query heads < 2^31,
- *   and an attention's launch less than 2^24 workgroups (B * heads of the cache is at most that); 1 <= width, width * page <= 2^30, 1 <= pages < 2^31. Arrays aligned to their element. Outputs and workspaces must not overlap inputs.
+ *   and an attention's launch less than 2^24 workgroups and 2^32 threads (it has more than B * heads of the cache workgroups,
+ *   of up to 512 threads); 1 <= width, width * page <= 2^30, 1 <= pages < 2^31. Arrays aligned to their element. Outputs and
+ *   workspaces must not overlap inputs.
  */
 typedef struct qpg_cache {
     void* k;

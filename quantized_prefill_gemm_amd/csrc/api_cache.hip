@@ -13,6 +13,8 @@ constexpr int64_t kMaxHeads = 4096;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxWords = 1024;
 constexpr int64_t kMaxInt = (int64_t)1 << 31;
+constexpr int64_t kMaxGroups = (int64_t)1 << 24;     // an attention's workgroups, which it divides as f32
+constexpr int64_t kMaxThreads = (int64_t)1 << 32;    // of a launch
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 bool type_ok(int t) { return t == QPG_F32 || t == QPG_F16 || t == QPG_BF16; }
@@ -55,7 +57,10 @@ int attention(const qpg_cache* cache, const qpg_batch* batch, const qpg_scores* 
     if (!isfinite(1.5f * scores->scale) || !isfinite(1.5f * scores->cap) ||
         (scores->cap > 0.0f && !isfinite(3.0f * scores->scale / scores->cap)))
         return QPG_EINVAL;
-    if (qpg_cache_attention_grid(batch->T, batch->B, heads, cache->heads, cache->dim, batch->width * cache->page) >= kMaxRows)
+    int64_t threads;
+    if (qpg_cache_attention_grid(batch->T, batch->B, heads, cache->heads, cache->dim, batch->width * cache->page, &threads) >=
+            kMaxGroups ||
+        threads >= kMaxThreads)
         return QPG_EINVAL;
     if (!ws && qpg_cache_attention_bytes(batch->T, batch->B, heads, cache->heads, cache->dim, batch->width * cache->page))
         return QPG_EINVAL;

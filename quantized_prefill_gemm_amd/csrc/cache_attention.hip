@@ -787,10 +787,12 @@ int qpg_cache_attention_splits(int64_t T, int64_t B, int64_t heads, int64_t kv, 
     return form_of(T, B, heads, kv, dim, length).splits;
 }
 
-int64_t qpg_cache_attention_grid(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length)
+int64_t qpg_cache_attention_grid(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length, int64_t* threads)
 {
     const AttentionForm f = form_of(T, B, heads, kv, dim, length);
-    return f.slots * kv * f.splits;
+    const int64_t grid = f.slots * kv * f.splits;
+    *threads = grid * 64 * f.wc * f.wk;
+    return grid;
 }
 
 hipError_t qpg_launch_cache_attention(const qpg_cache& cache, const qpg_batch& batch, const qpg_scores& scores,

@@ -46,8 +46,8 @@ hipError_t qpg_launch_cache_append(const qpg_cache& cache, const qpg_batch& batc
                                    const float* q_norm, const float* k_norm, float eps, void* y, hipStream_t s);
 // Number of pieces that the keys of a tile are split into (1: no workspace).
 int qpg_cache_attention_splits(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length);
-// Workgroups of the launch (its threads must be less than 2^32).
-int64_t qpg_cache_attention_grid(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length);
+// Workgroups of the launch (less than 2^24), and its threads (less than 2^32).
+int64_t qpg_cache_attention_grid(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length, int64_t* threads);
 hipError_t qpg_launch_cache_attention(const qpg_cache& cache, const qpg_batch& batch, const qpg_scores& scores,
                                       const void* q, int64_t heads, const int64_t* tree, int64_t words,
                                       const int32_t* positions, void* y, int y_type, void* ws, hipStream_t s);
