@@ -392,7 +392,8 @@ typedef struct qpg_scores {
  *   new ones, and node m iff bit m % 64 of word m / 64 of its row of `tree` (int64 [T][words]) is set: its ancestors and itself,
  *   in any order of the nodes.
  *   positions int32 [T], 0 .. 2^30, are the nodes' (the length before plus the depth), for window and slopes;
- *   nodes from 64 * words on are seen by none. 1 <= words <= 1024. prefix must be null.
+ *   nodes from 64 * words on are seen by none. 1 <= words <= 1024. prefix must be null. The nodes lie in the cache in
+ *   their order as rows; those of the accepted branch are appended again at their places, as the next call's new tokens.
  *   ws: qpg_cache_attention_bytes(T, B, heads, cache heads, dim, width * page) bytes, 16-byte aligned
  *   (null when 0); calls that share it must not overlap in time. One or two kernels are enqueued.
  */

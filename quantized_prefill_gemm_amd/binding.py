@@ -903,7 +903,8 @@ def cache_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
                          cap: float = 0.0, slopes=None, window: int = 0, y=None, ws=None, dtype=None, stream=None) -> torch.Tensor:
     """As cache_attention for a tree of drafted tokens: the new tokens of a sequence are nodes, which see every
     key before the new ones and the nodes m whose bit m % 64 of word m // 64 of their row of tree [T, words]
-    (int64) is set -- their ancestors and themselves. positions [T] int32: the nodes' (as given to cache_append)."""
+    (int64) is set -- their ancestors and themselves. positions [T] int32: the nodes', the length before the new ones plus
+    the depth (as given to cache_append)."""
     if tree is None or positions is None:
         raise QPGError(QPG_EINVAL, "tree and positions must be given")
     return _attention(q, k_cache, v_cache, table, lens, offsets, scale, cap, slopes, window, None, tree, positions, y, ws, dtype,

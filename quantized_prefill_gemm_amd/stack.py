@@ -255,7 +255,7 @@ class AttentionStack(Stack):
             to.copy_(t)
 
     def set_tree(self, tree: torch.Tensor, positions: torch.Tensor):
-        """Of a stack with `words`: which nodes each new token sees, and its position."""
+        """Of a stack with `words`: which nodes each new token sees, and its position (the length before plus its depth)."""
         if self.tree is None:
             raise ValueError("the stack was made without words for trees")
         self.tree.copy_(tree)
