@@ -386,8 +386,8 @@ typedef struct qpg_scores {
  *   the cache. Key j's position is j. Keys and values that a row does not see do not touch it, whatever they hold.
  *   Scores and sums are f32. The shares that multiply the values are rounded to the cache's type (half a
  *   step each); with a y_type of more bits than that they are two (f16) or three (bf16) pieces, which
- *   leave f32's own errors. A row that sees an infinite value is infinite or, where a piece of its share is 0 or less,
- *   NaN.
+ *   leave f32's own errors. A row that sees an infinite value is infinite there, of its sign, whatever its share, and NaN
+ *   where it sees both signs or a NaN; such values slow down the tiles that see them, or could have (two times and more).
  * cache_attention_tree: the new tokens of a sequence are nodes of a tree of drafts. A node sees the tokens before the
  *   new ones, and node m iff bit m % 64 of word m / 64 of its row of `tree` (int64 [T][words]) is set: its ancestors and itself,
  *   in any order of the nodes.

@@ -32,7 +32,6 @@ namespace qpg {
 typedef __attribute__((address_space(3))) void lds_void;
 typedef short shortx4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) shortx4 lds_shortx4;
-typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
 
 struct AttentionArgs {
     CacheBatch batch;
@@ -119,6 +118,9 @@ __device__ __forceinline__ float half_sum(float x)
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// x * s of an s that is 0 or more, where an infinite x stays.
+__device__ __forceinline__ float scaled(float x, float s) { return fabsf(x) == INFINITY ? x : x * s; }
+
 // n / d for 0 <= n < 2^24, 1 <= d: f32's quotient is off by one at most.
 __device__ __forceinline__ int divide(int n, int d)
 {
@@ -173,6 +175,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     constexpr int STAGE = AttentionLds<DP, KT, WK>::STAGE;
     constexpr size_t JOIN = WK > 1 ? (size_t)WC * WK * 32 * (DP * 4 + 8) : 0;      // groups joined: o, maxima and sums
     __shared__ __align__(1024) uint8_t lds_raw[sizeof(AttentionLds<DP, KT, WK>) > JOIN ? sizeof(AttentionLds<DP, KT, WK>) : JOIN];
+    __shared__ int lds_again;
     AttentionLds<DP, KT, WK>& lds = *reinterpret_cast<AttentionLds<DP, KT, WK>*>(lds_raw);
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -223,10 +226,10 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
 
     // This lane's column. Columns behind the last do as the last does, and are not written.
     const int token0 = c0 / a.group, spare = c0 - token0 * a.group;         // columns are token * group + head in group
-    auto token_of = [&](int i) { return token0 + divide(spare + i, a.group); };
+    auto token_of = [&](int i) __attribute__((always_inline)) { return token0 + divide(spare + i, a.group); };
     const int col = 32 * wc + l31, own = min(col, columns - 1);
     const int token = token_of(own), head = h * a.group + spare + own - (token - token0) * a.group;
-    auto position_of = [&](int t) {
+    auto position_of = [&](int t) __attribute__((always_inline)) {
         return a.tree ? min(max(a.positions[row0 + t], 0), 1 << 30) : ctx + t;
     };
     const int position = position_of(token);
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     const int head_stages = (min(prefix, end) + KT - 1) / KT;
     const int begin_stage = max(begin / KT, head_stages), end_stage = (end + KT - 1) / KT;
     const int stages = head_stages + max(end_stage - begin_stage, 0);
-    auto key_of = [&](int i) { return (i < head_stages ? i : i - head_stages + begin_stage) * KT; };
+    auto key_of = [&](int i) __attribute__((always_inline)) { return (i < head_stages ? i : i - head_stages + begin_stage) * KT; };
     const int share = max(((stages + a.splits - 1) / a.splits + WK - 1) / WK * WK, WK * a.least);
     const int i0 = min(split * share, stages), i1 = min(i0 + share, stages);
     const bool parts = stages > share;                 // else the first piece is all, and writes y
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         voff[j] = 8 * piece < a.dim ? (unsigned)((r & 15) * row_bytes + 16 * piece) : NOWHERE;
     }
     int pages[NB];
-    auto look_up = [&](int i) {
+    auto look_up = [&](int i) __attribute__((always_inline)) {
         const int key = i < i1 ? key_of(i) : 0;
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         }
     };
     const unsigned lds_k = (unsigned)(uintptr_t)(lds_void*)&lds.k[wk][0][0], lds_v = (unsigned)(uintptr_t)(lds_void*)&lds.v[wk][0][0];
-    auto load_stage = [&](int i, int buffer) {
+    auto load_stage = [&](int i, int buffer) __attribute__((always_inline)) {
         const int key = i < i1 ? key_of(i) : 1 << 30;
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
@@ -320,21 +323,16 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
     };
 
     floatx16 o[ND];
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
-    float m = FAR, sum = 0.0f;                         // m: in powers of two
-    bool odd = false;
+    float m, sum;                                      // m: in powers of two
 
     // The first seen key position of this column, the position of a key, and the seen ones of keys j .. j + 63 as bits
     // (of nodes without the window).
     const int from = a.window < NO_WINDOW ? position - a.window + 1 : -1;
     const float slope = a.slopes ? a.slopes[head] * LOG2E : 0.0f;
-    auto key_position = [&](int j) {
+    auto key_position = [&](int j) __attribute__((always_inline)) {
         return a.tree && j >= ctx ? position_of(min(j - ctx, news - 1)) : j;
     };
-    auto seen_from = [&](int j) {
+    auto seen_from = [&](int j) __attribute__((always_inline)) {
         auto range = [&](int lo, int hi) -> uint64_t {
             const int x = max(lo - j, 0), z = min(hi - j, 63);
             return z < x ? 0 : (~(uint64_t)0 << x) & (~(uint64_t)0 >> (63 - z));
@@ -362,235 +360,282 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         v_place[e] = (v_row + 8 * e) * DP * 2 + ((piece ^ swizzle<DP>(v_row + 8 * e)) << 4) + (i16 & 1) * 8;
     }
 
-    if (rounds > 0) {
-        look_up(i0 + wk);
-        load_stage(i0 + wk, 0);
-        look_up(i0 + wk + WK);
-    }
-    // The compiler's own loads end here, so that none of its waits in the loop is one for the stage under way.
+    // Values that are no numbers. Times a share of 0, a key's that is not seen, or times a piece of a share, they make NaN in
+    // the products. So a wave whose results hold a NaN in a row whose sum is a number walks its stages a second time, with care:
+    // of each stage that has landed such values are added to the rows that see them, whatever their shares, and
+    // then are 0 in LDS. One of them costs a tile a second walk (8192 tokens, one NaN in the last: 890 us for 540), and each stage that
+    // holds some 10 us and more; tiles whose results are numbers pay one multiplication a value at their end.
+    auto careful = [&](int i, int buffer) __attribute__((always_inline)) {
+        uint8_t* vb = lds.v[wk][buffer];
+        auto bad = [](uint32_t x) {                    // of two values: all bits of one that is no number
+            const uint32_t lo = (x & Matrix<T>::INF) == Matrix<T>::INF ? 0xFFFFu : 0;
+            const uint32_t hi = ((x >> 16) & Matrix<T>::INF) == Matrix<T>::INF ? 0xFFFF0000u : 0;
+            return lo | hi;
+        };
+        auto landed = [] {                             // what the waves of the stage read and wrote of it
+            if (WC > 1)
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        };
+        bool any = false;
+        if (i < i1) {
+#pragma unroll 1
+            for (int at = lane * 16; at < STAGE; at += 1024) {
+                const uint32x4 x = *reinterpret_cast<const uint32x4*>(vb + at);
+                any |= (bad(x[0]) | bad(x[1]) | bad(x[2]) | bad(x[3])) != 0;
+            }
+            any = __ballot(any) != 0;
+        }
+        if (any) {
+            const int key = key_of(i);
+            const uint64_t seen = seen_from(key);
+#pragma unroll 1
+            for (int j = 0; j < KT && key + j < n; ++j) {
+                const bool on = ((seen >> j) & 1) && (!a.tree || key_position(key + j) >= from);
 #pragma unroll
-    for (int t = 0; t < NK; ++t) {
-        if (DP == 256)                                 // kept in accumulation registers, which products read as well
-            asm volatile("" : "+a"(qt[t]));
-        else
-            asm volatile("" : "+v"(qt[t]));
-    }
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const Pack<T, 4> x = *reinterpret_cast<const Pack<T, 4>*>(
+                            vb + j * DP * 2 + (((4 * d + r) ^ swizzle<DP>(j)) << 4) + 8 * half);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float f = (float)x.v[e];
+                            if (on && !(fabsf(f) < INFINITY)) o[d][4 * r + e] += f;
+                        }
+                    }
+            }
+        }
+        landed();
+        if (any) {
+#pragma unroll 1
+            for (int at = wc * (STAGE / WC) + lane * 16; at < (wc + 1) * (STAGE / WC); at += 1024) {
+                uint32x4 x = *reinterpret_cast<const uint32x4*>(vb + at);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] &= ~bad(x[e]);
+                *reinterpret_cast<uint32x4*>(vb + at) = x;
+            }
+        }
+        landed();
+    };
+
+    if (WC > 1 && threadIdx.x == 0) lds_again = 0;     // (before the first barrier of a walk)
     // Stages whose keys every column of the wave sees, and whose scores are the products, take a short way.
     int plain_low = a.window < NO_WINDOW ? wave_high - a.window + 1 : 0, plain_high = min(wave_low, n - 1);
     if (a.tree) plain_low = a.window < NO_WINDOW ? high - a.window + 1 : 0, plain_high = min(ctx, n) - 1;
     if (a.slopes || a.cap > 0.0f) plain_high = -1;
-    for (int round = 0; round < rounds; ++round) {
-        const int i = i0 + wk + round * WK, buffer = round & 1;
-        // this stage has landed, and every wave is done with the other buffer
-        if (WC > 1)
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        if (round + 1 < rounds) {
-            load_stage(i + WK, buffer ^ 1);
-            look_up(i + 2 * WK);
-        }
-        if (i >= i1) continue;
-        const int key = key_of(i), last = key + KT - 1;
-        // a stage that none of the wave's columns sees
-        if (!a.tree && key >= prefix && (key > wave_high || last < wave_low - a.window + 1)) continue;
-
-        const uint8_t* kb = lds.k[wk][buffer];
-        const uint8_t* vb = lds.v[wk][buffer];
-        floatx16 s[NS];
-#pragma unroll
-        for (int e = 0; e < NS; ++e)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[e][r] = 0.0f;
-        // A block's operands are read while the block before it is multiplied.
-        auto keys = [&](int e, int t) { return *reinterpret_cast<const x8*>(kb + e * 32 * DP * 2 + (k_place ^ (t << 5))); };
-        x8 kf[NK];
-#pragma unroll
-        for (int t = 0; t < NK; ++t) kf[t] = keys(0, t);
-#pragma unroll
-        for (int e = 0; e < NS; ++e)
-#pragma unroll
-            for (int t = 0; t < NK; ++t) {
-                s[e] = Matrix<T>::mul(kf[t], qt[t], s[e]);
-                if (e + 1 < NS) kf[t] = keys(e + 1, t);
-            }
-        __builtin_amdgcn_sched_group_barrier(0x100, NK, 0);             // LDS reads
-#pragma unroll
-        for (int t = 0; t < (NS - 1) * NK; ++t) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // matrix
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, NK, 0);
-
-        float c = a.scale;                             // c * s are scores in powers of two
-        if (key < plain_low || last > plain_high) {
-            if (a.cap > 0.0f) {
-                c = 1.0f;
-                if (NP > 1 || a.cap > COARSE_CAP) {
-#pragma unroll
-                    for (int e = 0; e < NS; ++e)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) s[e][r] = capped(s[e][r], a.cap, a.cap_scale, true);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < NS; ++e)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) s[e][r] = capped(s[e][r], a.cap, a.cap_scale, false);
-                }
-            }
-            const bool whole = a.tree ? last < ctx && (a.window >= NO_WINDOW || high - key < a.window)
-                                      : last < n && (last < prefix || (last <= wave_low && wave_high - key < a.window));
-            // Node positions, where they matter, are fetched by the lanes together.
-            const bool placed = a.tree && last >= ctx && (a.slopes || a.window < NO_WINDOW);
-            int at_lane = 0;
-            if (placed) {
-                at_lane = key_position(key + lane);
-                asm volatile("" : "+v"(at_lane));          // its load ends here
-            }
-            if (a.slopes) {
-                const float gap = (float)(position - key - 4 * half);
-#pragma unroll
-                for (int e = 0; e < NS; ++e)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int i = 32 * e + 8 * (r >> 2) + (r & 3);
-                        float far = gap - (float)i;
-                        if (placed) far = (float)(position - __shfl(at_lane, i + 4 * half));
-                        s[e][r] = __builtin_fmaf(-slope, fabsf(far), s[e][r] * c);
-                    }
-                c = 1.0f;
-            }
-            if (!whole) {
-                const uint64_t seen = seen_from(key) >> (4 * half);        // bit i: key + 4 half + i is seen
-#pragma unroll
-                for (int e = 0; e < NS; ++e) {
-                    const uint32_t bits = (uint32_t)(seen >> (32 * e));
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int i = 8 * (r >> 2) + (r & 3);
-                        bool on = (bits >> i) & 1;
-                        if (placed) {
-                            const int at = __shfl(at_lane, 32 * e + i + 4 * half);         // by all lanes
-                            on = on && at >= from;
-                        }
-                        s[e][r] = on ? s[e][r] : -INFINITY;
-                    }
-                }
-                // A value that is no number times a share of 0 would be NaN. Rows that one column of the wave sees and
-                // another does not are looked through for such values; where there are any, the columns are done again below.
-                const int upto = min(last, n - 1);
-                const bool mixed = a.tree ? upto >= ctx || high - key >= a.window
-                                          : !(upto < prefix || (upto <= wave_low && wave_high - key < a.window));
-                if (mixed) {
-                    ushortx2 most = {0, 0};
-#pragma unroll 4
-                    for (int at = lane * 16; at < STAGE; at += 1024) {
-                        const uint32x4 x = *reinterpret_cast<const uint32x4*>(vb + at);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            most = __builtin_elementwise_max(most, __builtin_bit_cast(ushortx2, x[e] & 0x7FFF7FFFu));
-                    }
-                    odd |= __ballot(max(most[0], most[1]) >= Matrix<T>::INF) != 0;
-                }
-            }
-        }
-
-        // Running maximum. It is moved only when it has grown by 2^8 (8 bits of f32's, and f16's, range are spare).
-        float top = s[0][0];
-#pragma unroll
-        for (int e = 0; e < NS; ++e)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[e][r]);
-        top = half_max(top) * c;
-        if (__ballot(top > m + 8.0f)) {
-            const float next = fmaxf(m, top), shrink = __builtin_amdgcn_exp2f(m - next);
-            m = next;
-            sum *= shrink;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[d][r] *= shrink;
-        }
-        // V^T rows 32d .. 32d + 31, keys 16f + 4 half + 0..3 and + 8
-        auto values = [&](int f, int d) {
-            union { shortx4 s[2]; x8 v; } u;
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)(vb + f * 16 * DP * 2 + (v_place[e] ^ (d << 6))));
-            return u.v;
-        };
-        x8 vf[ND];
-#pragma unroll
-        for (int d = 0; d < ND; ++d) vf[d] = values(0, d);
-        const float base = (float)Matrix<T>::LIFT - m;
-        float part = 0.0f;
-#pragma unroll
-        for (int f = 0; f < 2 * NS; ++f) {
-            x8 p[NP];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float rest = __builtin_amdgcn_exp2f(__builtin_fmaf(s[f >> 1][8 * (f & 1) + i], c, base));
-                if (NP > 1) part += rest;
-#pragma unroll
-                for (int g = 0; g < NP; ++g) {
-                    const T piece = (T)rest;           // to nearest even; the next piece is what it left
-                    p[g][i] = piece;
-                    rest -= (float)piece;
-                }
-            }
-            if (NP == 1)                               // the sum of the shares as they are multiplied, two at a time
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part = Matrix<T>::sum2(p[0], i, part);
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-#pragma unroll
-                for (int g = 0; g < NP; ++g) o[d] = Matrix<T>::mul(vf[d], p[g], o[d]);
-                if (f + 1 < 2 * NS) vf[d] = values(f + 1, d);
-            }
-        }
-        sum += part;
-    }
-    if (odd) {
-        // Key by key, in f32: a value counts where its key is seen.
+    auto walk = [&](auto care) __attribute__((always_inline)) {
+        constexpr bool CARE = decltype(care)::value;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
         m = FAR, sum = 0.0f;
-#pragma unroll 1
-        for (int i = i0 + wk; i < i1; i += WK)
-#pragma unroll 1
-            for (int j = key_of(i); j < min(key_of(i) + KT, n); ++j) {
-                const int page = min(max(table[j >> a.page_bits], 0), a.pages - 1), in_page = j & ((1 << a.page_bits) - 1);
-                const T* kr = kc + page * a.k_page + (int64_t)in_page * a.dim;
-                const T* vr = vc + page * a.v_page + (int64_t)in_page * a.dim;
-                float x = 0.0f;
+        // The careful walk, which is rare, asks for its first stage in a round of its own: one place for its loads.
+        int round = CARE ? -1 : 0;
+        if constexpr (CARE) asm volatile("" : "+s"(round));
+        if (rounds > 0) {
+            look_up(i0 + wk);
+            if (!CARE) {
+                load_stage(i0 + wk, 0);
+                look_up(i0 + wk + WK);
+            }
+        }
+        // The compiler's own loads end here, so that none of its waits in the loop is one for the stage under way.
 #pragma unroll
-                for (int t = 0; t < NK; ++t)
-                    if (8 * (2 * t + half) < a.dim) {
-                        const x8 kv = *reinterpret_cast<const x8*>(kr + 8 * (2 * t + half));
+        for (int t = 0; t < NK; ++t) {
+            if (DP == 256)                                 // kept in accumulation registers, which products read as well
+                asm volatile("" : "+a"(qt[t]));
+            else
+                asm volatile("" : "+v"(qt[t]));
+        }
+        for (; round < rounds; ++round) {
+            const int i = i0 + wk + round * WK, buffer = round & 1;
+            // this stage has landed, and every wave is done with the other buffer
+            if (WC > 1)
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            if (CARE && round >= 0) careful(i, buffer);
+            if (round + 1 < rounds) {
+                load_stage(i + WK, buffer ^ 1);
+                look_up(i + 2 * WK);
+            }
+            if (i >= i1 || (CARE && round < 0)) continue;
+            const int key = key_of(i), last = key + KT - 1;
+            // a stage that none of the wave's columns sees
+            if (!a.tree && key >= prefix && (key > wave_high || last < wave_low - a.window + 1)) continue;
+
+            const uint8_t* kb = lds.k[wk][buffer];
+            const uint8_t* vb = lds.v[wk][buffer];
+            floatx16 s[NS];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x += (float)kv[e] * (float)qt[t][e];
+            for (int e = 0; e < NS; ++e)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[e][r] = 0.0f;
+            // A block's operands are read while the block before it is multiplied.
+            auto keys = [&](int e, int t) { return *reinterpret_cast<const x8*>(kb + e * 32 * DP * 2 + (k_place ^ (t << 5))); };
+            x8 kf[NK];
+#pragma unroll
+            for (int t = 0; t < NK; ++t) kf[t] = keys(0, t);
+#pragma unroll
+            for (int e = 0; e < NS; ++e)
+#pragma unroll
+                for (int t = 0; t < NK; ++t) {
+                    s[e] = Matrix<T>::mul(kf[t], qt[t], s[e]);
+                    if (e + 1 < NS) kf[t] = keys(e + 1, t);
+                }
+            __builtin_amdgcn_sched_group_barrier(0x100, NK, 0);             // LDS reads
+#pragma unroll
+            for (int t = 0; t < (NS - 1) * NK; ++t) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // matrix
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, NK, 0);
+
+            float c = a.scale;                             // c * s are scores in powers of two
+            if (key < plain_low || last > plain_high) {
+                if (a.cap > 0.0f) {
+                    c = 1.0f;
+                    if (NP > 1 || a.cap > COARSE_CAP) {
+#pragma unroll
+                        for (int e = 0; e < NS; ++e)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) s[e][r] = capped(s[e][r], a.cap, a.cap_scale, true);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < NS; ++e)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) s[e][r] = capped(s[e][r], a.cap, a.cap_scale, false);
                     }
-                x = half_sum(x);
-                x = a.cap > 0.0f ? capped(x, a.cap, a.cap_scale, true) : x * a.scale;
-                const int at = key_position(j);
-                if (a.slopes) x -= slope * fabsf((float)(position - at));
-                if (!(seen_from(j) & 1) || (a.tree && at < from)) continue;
-                const float next = fmaxf(m, x), shrink = __builtin_amdgcn_exp2f(m - next);
-                const float p = __builtin_amdgcn_exp2f(x - next);
+                }
+                const bool whole = a.tree ? last < ctx && (a.window >= NO_WINDOW || high - key < a.window)
+                                          : last < n && (last < prefix || (last <= wave_low && wave_high - key < a.window));
+                // Node positions, where they matter, are fetched by the lanes together.
+                const bool placed = a.tree && last >= ctx && (a.slopes || a.window < NO_WINDOW);
+                int at_lane = 0;
+                if (placed) {
+                    at_lane = key_position(key + lane);
+                    asm volatile("" : "+v"(at_lane));          // its load ends here
+                }
+                if (a.slopes) {
+                    const float gap = (float)(position - key - 4 * half);
+#pragma unroll
+                    for (int e = 0; e < NS; ++e)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int i = 32 * e + 8 * (r >> 2) + (r & 3);
+                            float far = gap - (float)i;
+                            if (placed) far = (float)(position - __shfl(at_lane, i + 4 * half));
+                            s[e][r] = __builtin_fmaf(-slope, fabsf(far), s[e][r] * c);
+                        }
+                    c = 1.0f;
+                }
+                if (!whole) {
+                    const uint64_t seen = seen_from(key) >> (4 * half);        // bit i: key + 4 half + i is seen
+#pragma unroll
+                    for (int e = 0; e < NS; ++e) {
+                        const uint32_t bits = (uint32_t)(seen >> (32 * e));
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int i = 8 * (r >> 2) + (r & 3);
+                            bool on = (bits >> i) & 1;
+                            if (placed) {
+                                const int at = __shfl(at_lane, 32 * e + i + 4 * half);         // by all lanes
+                                on = on && at >= from;
+                            }
+                            s[e][r] = on ? s[e][r] : -INFINITY;
+                        }
+                    }
+                }
+            }
+
+            // Running maximum. It is moved only when it has grown by 2^8 (8 bits of f32's, and f16's, range are spare).
+            float top = s[0][0];
+#pragma unroll
+            for (int e = 0; e < NS; ++e)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[e][r]);
+            top = half_max(top) * c;
+            if (__ballot(top > m + 8.0f)) {
+                const float next = fmaxf(m, top), shrink = __builtin_amdgcn_exp2f(m - next);
                 m = next;
-                sum = sum * shrink + p;
+                sum *= shrink;
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int row = 32 * d + 8 * (r >> 2) + 4 * half + (r & 3);
-                        o[d][r] = o[d][r] * shrink + (row < a.dim ? p * (float)vr[row] : 0.0f);
-                    }
+                    for (int r = 0; r < 16; ++r) o[d][r] = CARE ? scaled(o[d][r], shrink) : o[d][r] * shrink;
             }
-        m += (float)Matrix<T>::LIFT;
-        sum = half == 0 ? sum : 0.0f;                  // both halves have it whole
+            // V^T rows 32d .. 32d + 31, keys 16f + 4 half + 0..3 and + 8
+            auto values = [&](int f, int d) {
+                union { shortx4 s[2]; x8 v; } u;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)(vb + f * 16 * DP * 2 + (v_place[e] ^ (d << 6))));
+                return u.v;
+            };
+            x8 vf[ND];
+#pragma unroll
+            for (int d = 0; d < ND; ++d) vf[d] = values(0, d);
+            const float base = (float)Matrix<T>::LIFT - m;
+            float part = 0.0f;
+#pragma unroll
+            for (int f = 0; f < 2 * NS; ++f) {
+                x8 p[NP];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float rest = __builtin_amdgcn_exp2f(__builtin_fmaf(s[f >> 1][8 * (f & 1) + i], c, base));
+                    if (NP > 1) part += rest;
+#pragma unroll
+                    for (int g = 0; g < NP; ++g) {
+                        // To nearest even; the next piece is what it left. One piece where y has no more bits than the cache:
+                        // half a step of each share, where y's own rounding is half a step of their sum. Every further
+                        // piece is one more product over V (1024 tokens MHA: f16 one 27.4 us, two 33.9; bf16 one
+                        // 26.7, three 36.9; 8192 GQA bf16 531 and 925).
+                        const T piece = (T)rest;
+                        p[g][i] = piece;
+                        rest -= (float)piece;
+                    }
+                }
+                if (NP == 1)                               // the sum of the shares as they are multiplied, two at a time
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) part = Matrix<T>::sum2(p[0], i, part);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+#pragma unroll
+                    for (int g = 0; g < NP; ++g) o[d] = Matrix<T>::mul(vf[d], p[g], o[d]);
+                    if (f + 1 < 2 * NS) vf[d] = values(f + 1, d);
+                }
+            }
+            sum += part;
+        }
+    };
+    walk(std::false_type());
+    bool strange = false;                              // a result of the wave is no number
+    if (rounds > 0) {
+        float zero = 0.0f;                             // NaN where one is
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) zero = __builtin_fmaf(o[d][r], 0.0f, zero);
+        strange = __ballot(zero != zero) != 0;
+        bool care = false;
+        if (__builtin_expect(strange, false)) {
+            bool none = false;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) none |= o[d][r] != o[d][r];
+            const float total = half_sum(sum);
+            care = __ballot(none && total == total) != 0;
+        }
+        if constexpr (WC > 1) {                        // waves that share stages do them again together
+            if (care && lane == 0) lds_again = 1;
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            care = __builtin_amdgcn_readfirstlane(lds_again) != 0;
+        }
+        if (__builtin_expect(care, false)) walk(std::true_type());
     }
     m -= (float)Matrix<T>::LIFT;                       // sum and o are of powers relative to this
     sum = half_sum(sum);
@@ -606,7 +651,7 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
         float top = m;
 #pragma unroll
         for (int g = 0; g < WK; ++g) top = fmaxf(top, ml[(g * WC + wc) * 32 + l31][0]);
-        const float shrink = __builtin_amdgcn_exp2f(m - top);
+        float shrink = __builtin_amdgcn_exp2f(m - top);
         sum = 0.0f;
 #pragma unroll
         for (int g = 0; g < WK; ++g) {
@@ -614,6 +659,13 @@ __global__ void __launch_bounds__(64 * WC * WK, DP == 256 || WK > 1 ? 1 : 2) cac
             sum += x[1] * __builtin_amdgcn_exp2f(x[0] - top);
         }
         m = top;
+        if (__builtin_expect(strange, false) && shrink == 0.0f) {        // an infinite value stays
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[d][r] = scaled(o[d][r], 0.0f);
+            shrink = 1.0f;
+        }
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -708,14 +760,14 @@ __global__ void __launch_bounds__(256) cache_attention_join_kernel(const float* 
         m = next;
         sum *= shrink;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] *= shrink;
+        for (int e = 0; e < 4; ++e) o[e] = scaled(o[e], shrink);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (ml[i][1] == 0.0f) continue;            // an empty piece: o is not written
             const float w = __builtin_amdgcn_exp2f(ml[i][0] - m);
             sum += w * ml[i][1];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] += w * z[i][e];
+            for (int e = 0; e < 4; ++e) o[e] = fabsf(z[i][e]) == INFINITY ? o[e] + z[i][e] : __builtin_fmaf(w, z[i][e], o[e]);
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;

@@ -118,9 +118,8 @@ def compare(form, kind, y, cap=0.0, bias=False, window=0, prefix=None, tree=None
             want, bound = one_head(q[at:at + n, h], keys[:, h // group], values[:, h // group], see, far, kind, y, scale, cap, slope)
             mine, fine = got[at:at + n, h], torch.isfinite(want)
             assert torch.equal(torch.isfinite(mine), fine)
-            # a share in several pieces, one of them 0 or below, times an infinite value is NaN
             inf = torch.isinf(want)
-            assert bool(((mine[inf] == want[inf]) | torch.isnan(mine[inf])).all()) and bool(torch.isnan(mine[torch.isnan(want)]).all())
+            assert torch.equal(mine[inf], want[inf]) and bool(torch.isnan(mine[torch.isnan(want)]).all())
             over = ((mine - want).abs() - bound)[fine]
             assert float(over.max()) <= 0, (h, float(over.max()))
             strange += int((~fine).sum())

@@ -80,3 +80,55 @@ def test_no_wait_for_the_stage_under_way(kernels):
         at = max(i for i, x in enumerate(body) if x.startswith("buffer_load") and x.endswith(" lds"))
         upto = next(i for i in range(at, len(body)) if "mfma" in body[i])
         assert not any("vmcnt" in x for x in body[at:upto]), k
+
+
+@pytest.fixture(scope="module")
+def whole(kernels, tmp_path_factory):
+    """The attention kernels to their last instruction (a walk may lie behind the first s_endpgm)."""
+    path = next(p for p in sorted(tmp_path_factory.getbasetemp().glob("asm*/cache_attention.s")))
+    text, out = path.read_text(), {}
+    for name in kernels:
+        if "cache_attention_kernel" in name:
+            body = text[text.index("\n" + name + ":"):text.index(".amdhsa_kernel " + name)]
+            lines = [x.strip() for x in body.split("\n")]
+            out[name] = [x for x in lines if x and x[0] not in ";." and not x.endswith(":")]
+    return out
+
+
+def is_load(x):
+    return x.startswith("buffer_load") and x.endswith(" lds")
+
+
+def test_loads_of_both_walks_wait_for_their_scalars(whole):
+    """As above, to the last load of a kernel."""
+    loads = 0
+    for k, body in whole.items():
+        for i, x in enumerate(body):
+            if not is_load(x):
+                continue
+            loads += 1
+            lo, hi = map(int, re.search(r"s\[(\d+):(\d+)\]", x).groups())
+            states = 0
+            for y in reversed(body[max(0, i - 12):i]):
+                if states >= 5:
+                    break
+                m = re.match(r"v_read(?:first)?lane_b32 s(\d+)", y)
+                assert not (m and lo <= int(m.group(1)) <= hi), (k, y, x, states)
+                assert not (states < 1 and re.match(r"s_\w+ m0,", y)), (k, y, x)
+                states += int(y.split()[1]) + 1 if y.startswith("s_nop") else 1
+    assert loads > 1000
+
+
+def test_no_wait_for_the_stage_under_way_in_either_walk(whole):
+    """From a round's last load to its first product nothing waits for vector memory, once in each walk. (Behind the loads
+    of the first stage, before the loop, the queries are waited for.)"""
+    for k, body in whole.items():
+        walks, under_way = 0, False
+        for x in body:
+            if is_load(x):
+                under_way = True
+            elif x.startswith("s_waitcnt") and "vmcnt" in x:
+                under_way = False
+            elif "mfma" in x and under_way:
+                walks, under_way = walks + 1, False
+        assert walks == 2, (k, walks)
