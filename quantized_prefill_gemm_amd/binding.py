@@ -868,6 +868,10 @@ def _attention(q, k_cache, v_cache, table, lens, offsets, scale, cap, slopes, wi
     if ws is not None:
         _out(ws, torch.uint8, "ws", nws, k_cache)
     scores = _Scores(1.0 / math.sqrt(dim) if scale is None else scale, cap, _at(slopes), window, _at(prefix))
+    if cap and not scores.cap:                 # no cap would be what the library is asked for
+        raise QPGError(QPG_EINVAL, f"cap {cap} is 0 in float32")
+    if window != scores.window:
+        raise QPGError(QPG_EINVAL, f"a window of {window}")
 
     def call(s):
         out = q.new_empty(shape, dtype=dtype) if y is None else y
