@@ -362,7 +362,7 @@ typedef struct qpg_batch {
  *   s = scale * <q, k>;  cap > 0: s = cap * tanh(s / cap);  slopes (f32 [query heads] or null): s -= slopes[h] * |i - j|
  * and which keys a query sees: j <= i and, with window > 0, i - j < window; with prefix (int32 [B] or null) also every
  * j < prefix[b]. (prefix = lens: every query sees the whole sequence.) scale > 0, cap >= 0, window >= 0; 1.5 * scale,
- * 1.5 * cap and 3 * scale / cap finite.
+ * 3 * cap and 3 * scale / cap finite.
  */
 typedef struct qpg_scores {
     float scale, cap;

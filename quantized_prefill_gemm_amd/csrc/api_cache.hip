@@ -54,7 +54,7 @@ int attention(const qpg_cache* cache, const qpg_batch* batch, const qpg_scores* 
         scores->window < 0)
         return QPG_EINVAL;
     // the kernel's factors, in powers of two
-    if (!isfinite(1.5f * scores->scale) || !isfinite(1.5f * scores->cap) ||
+    if (!isfinite(1.5f * scores->scale) || !isfinite(3.0f * scores->cap) ||
         (scores->cap > 0.0f && !isfinite(3.0f * scores->scale / scores->cap)))
         return QPG_EINVAL;
     int64_t threads;
