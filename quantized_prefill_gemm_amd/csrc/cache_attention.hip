@@ -19,7 +19,7 @@
 // end: zeros. A 16-row block lies in one page, and has its own descriptor: 64-bit page addresses.
 //
 // Long prompts are bound by the vector arithmetic and the matrix instructions together, which hardly overlap in a wave:
-// 8192 tokens of 32 query over 8 heads of 128 in bf16 525 us, 1.05 PFLOP/s, the matrix units busy 54 % of the time and
+// 8192 tokens of 32 query over 8 heads of 128 in bf16 530 to 545 us by machine, 1.01 to 1.04 PFLOP/s, the matrix units busy 54 % of the time and
 // the vector units 48 % (powers are a quarter of a step's vector cycles), no LDS conflicts. (A pipeline of 32-key steps, one's K Q^T
 // among the powers of the one before, came to 557 to 619.) Decoding is bound by memory: 64 tokens over 130 to
 // 8100 of 8 heads 190 us, 5.5 TB/s. Few tiles are bound by the time of a tile's rounds, about 1.1 us each and 2.6
@@ -799,7 +799,10 @@ struct AttentionForm {
 //     64 38.8, of 128 48.9)
 //   pieces until there are about 128 workgroups, since joining them costs 3 us and more (one token over 4096, MHA: one
 //     piece 41, two 28.6, four 21.4, eight 22.2), and four where long caches would leave CUs without work at the end
-//     (64 tokens over up to 8100 GQA: one piece 203, two 196, four 190, eight 219). A piece has at least 256 keys.
+//     (64 tokens over up to 8100 GQA: one piece 203, two 196, four 190, eight 219). A piece has at least 256 keys. One
+//     piece against four, 200 to 8000 tokens: 64 GQA 213, 203; 128 GQA 388, 381; 16 MHA 208, 182; 100 of 16 over 4 heads of 64
+//     106, 88; 64 of 16 over 8 of 256 425, 382. They cost where lengths are alike (64 over 4100 184, 203; 16 47, 52), and
+//     where the table is far longer than they are (64 over 200 to 1000 34, 67; 32 over 2000 48, 60).
 AttentionForm form_of(int64_t T, int64_t B, int64_t heads, int64_t kv, int64_t dim, int64_t length)
 {
     const int64_t group = heads / kv, busy = B < T ? B : T, mean = (T * group + busy - 1) / busy;
